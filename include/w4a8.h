@@ -318,6 +318,50 @@ w4a8_status w4a16_gemm(const uint16_t* a_dev, int lda, int m, int k,
  * the call would be rejected.  Host only, no HIP call. */
 int w4a8_linear_launches(int m, int n, int k, int g, const w4a8_gemm_opts* opts);
 
+/* --------------------------------------------- int8 inputs of the linears
+ * Two operators of a decoder layer that produce a linear layer's int8 input
+ * directly, so that no fp16 copy of it is written: their a8 / s_a go to
+ * w4a8_gemm as they are.  Values are taken in fp32 from the fp16 inputs and
+ * quantized per token as in w4a8_quant_act:
+ *   s_a[m] = fp16(max_k |y[m,k]| / 127),
+ *   A8 = clamp(rint(y * fp32(1/s_a)), -127, 127)   (0 where s_a == 0)
+ * Rows of any k from 1 to W4A8_ACT_K_MAX and any row strides >= k; rows whose
+ * pointers are 16-byte aligned (a8: 8), with strides and k multiples of 8,
+ * take 16-byte loads.  m == 0 is a no-op. */
+
+/* Root-mean-square norm with the residual's addition:
+ *   h = fp16(x + residual)                (h = x without a residual)
+ *   y = h * weight / sqrt(mean_k(h^2) + eps)
+ *   residual_dev  m x k fp16, or NULL
+ *   weight_dev    k fp16
+ *   h_dev         m x k fp16, the new residual stream: required with a
+ *                 residual, optional (may be NULL, then not written) without.
+ *                 It may be x_dev or residual_dev (same stride).
+ * The norm is taken of the rounded h, the value the next layer's residual
+ * addition reads.  A row whose h holds a NaN or an infinity gets s_a = NaN, so
+ * that what the linear makes of it is NaN as well (its codes are
+ * unspecified); a non-finite weight gives unspecified outputs.
+ * Errors: INVALID_ARGUMENT (null pointer, m < 0, k <= 0, a stride < k, eps
+ * negative or not finite, a residual without h_dev, m > W4A8_M_MAX,
+ * k > W4A8_ACT_K_MAX), DEVICE. */
+w4a8_status w4a8_rms_norm_quant(const uint16_t* x_dev, int ldx,
+                                const uint16_t* residual_dev, int ldr,
+                                const uint16_t* weight_dev, float eps, int m, int k,
+                                uint16_t* h_dev, int ldh, int8_t* a8_dev, int lda8,
+                                uint16_t* s_a_dev, void* stream);
+
+/* The gated activation in front of the down projection:
+ *   y = gate / (1 + exp(-gate)) * up
+ * gate_dev and up_dev are m x k fp16 with strides of their own, so the two
+ * halves of one gate-and-up output serve as they are (up_dev = gate_dev + k,
+ * both strides 2k).  A row with a NaN (or infinity * 0) in y gets s_a = NaN.
+ * Errors: INVALID_ARGUMENT (null pointer, m < 0, k <= 0, a stride < k,
+ * m > W4A8_M_MAX, k > W4A8_ACT_K_MAX), DEVICE. */
+w4a8_status w4a8_silu_mul_quant(const uint16_t* gate_dev, int ldg,
+                                const uint16_t* up_dev, int ldu, int m, int k,
+                                int8_t* a8_dev, int lda8, uint16_t* s_a_dev,
+                                void* stream);
+
 /* ------------------------------------------------------- measurement aid
  * Not part of the layer.  A read-only stream over `bytes` of device memory
  * (16-byte aligned, a multiple of 16) by `workgroups` x 512 threads, with

@@ -79,6 +79,8 @@ def _load():
         "w4a8_linear_launches": (I, [I, I, I, I, P]),
         "w4a16_gemm": (I, [P, I, I, I, P, I, I, P, I, P, P]),
         "w4a8_read_probe": (I, [P, Z, I, P, P]),
+        "w4a8_rms_norm_quant": (I, [P, I, P, I, P, ctypes.c_float, I, I, P, I, P, I, P, P]),
+        "w4a8_silu_mul_quant": (I, [P, I, P, I, I, I, P, I, P, P]),
         "w4a8_gemm_noalloc": (I, [P, I, P, I, P, I, I, I, P, I, P, I, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -303,6 +305,81 @@ def w4a16(a, blob_dev, n: int, k: int, g: int, y=None, variant: int = 0, k_split
                           ctypes.byref(opts) if opts is not None else None, _stream_ptr(stream)),
            "w4a16_gemm")
     return y
+
+
+def _rows(name, t, dtype, m=None, k=None):
+    """Check a 2-D CUDA tensor whose rows are contiguous."""
+    if t.dtype is not dtype or not t.is_cuda or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name}: expected a 2-D {dtype} CUDA tensor with contiguous rows")
+    if m is not None and (t.shape[0] != m or t.shape[1] != k):
+        raise ValueError(f"{name}: expected shape ({m}, {k}), got {tuple(t.shape)}")
+
+
+def _int8_out(m, k, a8, s_a, device):
+    """The outputs of a per-token quantizer, allocated where not given."""
+    torch = _torch()
+    if a8 is None:
+        a8 = torch.empty((m, k), dtype=torch.int8, device=device)
+    else:
+        _rows("a8", a8, torch.int8, m, k)
+    if s_a is None:
+        s_a = torch.empty((m,), dtype=torch.float16, device=device)
+    elif (s_a.dtype is not torch.float16 or not s_a.is_cuda or s_a.shape != (m,)
+          or not s_a.is_contiguous()):
+        raise ValueError(f"s_a: expected a contiguous float16 CUDA tensor of {m} values")
+    return a8, s_a
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor (a single row's stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def rms_norm_quant(x, weight, eps: float = 1e-5, residual=None, h=None, a8=None, s_a=None,
+                   stream=None):
+    """h = x + residual, then the RMS norm of h quantized per token: returns
+    (h, a8, s_a), a8 and s_a ready for gemm().  Without a residual h is x.
+    h may be given, also as x or residual themselves (in place)."""
+    torch = _torch()
+    _rows("x", x, torch.float16)
+    m, k = x.shape
+    if weight.dtype is not torch.float16 or weight.shape != (k,) or not weight.is_contiguous() \
+            or not weight.is_cuda:
+        raise ValueError(f"weight: expected a contiguous float16 CUDA tensor of {k} values")
+    if residual is not None:
+        _rows("residual", residual, torch.float16, m, k)
+        if h is None:
+            h = torch.empty((m, k), dtype=torch.float16, device=x.device)
+    if h is not None:
+        _rows("h", h, torch.float16, m, k)
+    a8, s_a = _int8_out(m, k, a8, s_a, x.device)
+    _check(lib.w4a8_rms_norm_quant(
+        x.data_ptr(), _ld(x), residual.data_ptr() if residual is not None else None,
+        _ld(residual) if residual is not None else 0, weight.data_ptr(), eps, m, k,
+        h.data_ptr() if h is not None else None, _ld(h) if h is not None else 0,
+        a8.data_ptr(), _ld(a8), s_a.data_ptr(), _stream_ptr(stream)), "w4a8_rms_norm_quant")
+    return (h if h is not None else x), a8, s_a
+
+
+def silu_mul_quant(gate, up=None, a8=None, s_a=None, stream=None):
+    """silu(gate) * up quantized per token: returns (a8, s_a).  With gate alone,
+    its left half is the gate and its right half up (one gate-and-up output)."""
+    torch = _torch()
+    _rows("gate", gate, torch.float16)
+    if up is None:
+        if gate.shape[1] % 2:
+            raise ValueError("gate: expected an even number of columns (gate and up side by side)")
+        m, k = gate.shape[0], gate.shape[1] // 2
+        up_ptr, ldu = gate.data_ptr() + 2 * k, _ld(gate)
+    else:
+        m, k = gate.shape
+        _rows("up", up, torch.float16, m, k)
+        up_ptr, ldu = up.data_ptr(), _ld(up)
+    a8, s_a = _int8_out(m, k, a8, s_a, gate.device)
+    _check(lib.w4a8_silu_mul_quant(gate.data_ptr(), _ld(gate), up_ptr, ldu, m, k, a8.data_ptr(),
+                                   _ld(a8), s_a.data_ptr(), _stream_ptr(stream)),
+           "w4a8_silu_mul_quant")
+    return a8, s_a
 
 
 def read_probe(buf, offset: int, nbytes: int, workgroups: int, sink, stream=None):

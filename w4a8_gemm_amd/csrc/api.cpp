@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "../../include/w4a8.h"
+#include "decoder_kernels.h"
 #include "kernels.h"
 #include "layout.h"
 
@@ -18,11 +19,16 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 thread_local hipError_t t_last_hip_error = hipSuccess;
 
-w4a8_status device_status(hipError_t e) {
+}  // namespace
+
+// shared with decoder_api.cpp
+w4a8_status w4a8::device_status(hipError_t e) {
   if (e == hipSuccess) return W4A8_OK;
   t_last_hip_error = e;
   return W4A8_ERR_DEVICE;
 }
+
+namespace {
 
 bool gemm_shape_supported(int n, int k, int g) {
   if (n % kColTile || k % kKBlock || k > W4A8_K_MAX || n > W4A8_N_MAX) return false;
