@@ -362,6 +362,116 @@ w4a8_status w4a8_silu_mul_quant(const uint16_t* gate_dev, int ldg,
                                 int8_t* a8_dev, int lda8, uint16_t* s_a_dev,
                                 void* stream);
 
+/* ---------------------------------------------------- paged int8 KV cache
+ * Keys and values of past tokens in pages of page_size token slots, int8
+ * with one fp16 scale for each (page, keys or values, kv head):
+ *   data   [num_pages][2][kv_heads][page_size][head_dim] int8 (0: keys,
+ *          1: values), pages page_stride bytes apart
+ *   scale  [num_pages][2][kv_heads] fp16, pages scale_stride values apart
+ * A value is code * scale.  Strides larger than a page let the layers of a
+ * model share one allocation.  The pool needs no initialisation.
+ *
+ * A batch of sequences with new tokens is described by
+ *   block_table  [batch][block_table_ld] int32: entry (b, i) is the page that
+ *                holds positions [i * page_size, (i + 1) * page_size) of
+ *                sequence b; the first max_pages entries of a row count
+ *   seq_lens     [batch] int32: tokens of each sequence with its new ones
+ *   cu_q         [batch + 1] int32: sequence b's new tokens are the rows
+ *                [cu_q[b], cu_q[b + 1]) of q, k, v and of the outputs, the
+ *                last at position seq_lens[b] - 1; cu_q[0] = 0, ascending,
+ *                cu_q[batch] = total_q.  NULL: one new token each
+ *                (total_q == batch).
+ * These tables are read on the device when the kernels run.  Whatever they
+ * hold, nothing outside the pool and the rows is read or written: lengths are
+ * clamped to max_pages * page_size, offsets to total_q, page numbers outside
+ * [0, num_pages) count as absent (nothing is written there, its keys are not
+ * seen).  Apart from absent pages such contents give unspecified results. */
+#define W4A8_HEAD_DIM_MAX 256
+#define W4A8_HEADS_MAX 4096
+typedef struct {
+  int8_t* data_dev;            /* 16-byte aligned */
+  uint16_t* scale_dev;
+  long long page_stride;       /* bytes, a multiple of 16, >= 2 * kv_heads * page_size * head_dim */
+  long long scale_stride;      /* fp16 values, >= 2 * kv_heads */
+  int num_pages;
+  int page_size;               /* 16, 32, 64, ... 1024 */
+  int kv_heads;
+  int head_dim;                /* a multiple of 16 up to W4A8_HEAD_DIM_MAX */
+  const int32_t* block_table_dev;
+  int block_table_ld;          /* >= max_pages */
+  int max_pages;               /* max_pages * page_size < 2^31 - page_size */
+  const int32_t* seq_lens_dev;
+  const int32_t* cu_q_dev;     /* may be NULL */
+  int batch;
+  int total_q;
+} w4a8_kv_view;
+
+/* Rotary positions on the new tokens' queries and keys, and their keys and
+ * values appended to the cache, in one launch.
+ *   pair (a, b) at angle index i:  (a cos - b sin, b cos + a sin)
+ *   half layout         a = x[i], b = x[i + rotary_dim / 2]
+ *   interleaved layout  a = x[2i], b = x[2i + 1]
+ * with cos = cos_sin[pos][i], sin = cos_sin[pos][rotary_dim / 2 + i], so that
+ * any frequencies and long-context scalings are the table's; values from
+ * rotary_dim on stay as they are.
+ *   q_dev, k_dev, v_dev   rows of q_heads * head_dim and kv_heads * head_dim
+ *                fp16, strides of their own (the parts of one QKV output)
+ *   cos_sin_dev  [max_pos][rotary_dim] fp32, 16-byte aligned; positions beyond
+ *                max_pos - 1 take its last row.  May be NULL if rotary_dim is 0.
+ *   rotary_dim   a multiple of 16 from 0 to head_dim
+ *   q_out_dev    rotated queries, fp16; may be q_dev (same stride)
+ * Rotation and quantization are fp32 on the fp16 inputs: keys are rounded
+ * once, to int8.  For every (page, keys or values, kv head) that gets new
+ * tokens, with s the scale it has, if slots before the first new one are in
+ * use, else 0:
+ *   s' = max(s, fp16(amax of the new values / 127))
+ *   old codes (only if s' > s): rint(code * fp32(s / s'))
+ *   new codes: clamp(rint(v * fp32(1 / s')), -127, 127)   (0 where s' == 0)
+ * so a page's scale grows with its tokens, and each time it does the codes
+ * before are off by at most half a step more.  A NaN or infinity among the new
+ * values makes the block's scale NaN or infinite, and what is read from it NaN.
+ * No page may be written by two sequences of one call.
+ * Rows are 16-byte aligned with strides a multiple of 8.  batch or total_q
+ * of 0 is a no-op.
+ * Errors: INVALID_ARGUMENT (null or misaligned pointer, stride too small, bad
+ * size), UNSUPPORTED (head_dim, page_size, rotary_dim, more than
+ * W4A8_HEADS_MAX heads), DEVICE. */
+w4a8_status w4a8_rope_append(const uint16_t* q_dev, int ldq, const uint16_t* k_dev, int ldk,
+                             const uint16_t* v_dev, int ldv, int q_heads,
+                             const float* cos_sin_dev, int rotary_dim, int max_pos,
+                             int interleaved, const w4a8_kv_view* view,
+                             uint16_t* q_out_dev, int ldqo, void* stream);
+
+/* Attention of the new tokens' queries over the cache (which holds the new
+ * tokens already: w4a8_rope_append first):
+ *   o = sum_t softmax_t(scale * q . k_t) v_t
+ * over the positions t <= pos of the sequence (its query's own position),
+ * and t > pos - window where window > 0.  Query head h reads kv head
+ * h / (q_heads / kv_heads).  A row that sees no key is 0.
+ *   q_dev, out_dev  rows of q_heads * head_dim fp16, 16-byte aligned, strides
+ *                   a multiple of 8
+ *   max_q, max_len  the most new tokens of one sequence and the longest
+ *                   sequence the caller expects (its host-side bounds): they
+ *                   choose the kernel, the split of long sequences and so the
+ *                   workspace.  Results stay right where the device's tables
+ *                   hold more, only slower.
+ *   workspace_dev   16-byte aligned, w4a8_paged_attention_workspace_size(view,
+ *                   q_heads, max_q, max_len) bytes (host only; pointers in the view
+ *                   are only checked for null); may be NULL when that is 0.
+ *                   No initialisation; calls in flight at once need one each.
+ * Scores, softmax statistics and sums are fp32; the softmax weights enter the
+ * second product as fp16.  Results do not depend on scheduling (no atomics).
+ * batch or total_q of 0 is a no-op.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (as w4a8_rope_append; q_heads not a
+ * multiple of kv_heads; total_q * q_heads >= 2^31), BUFFER_TOO_SMALL,
+ * DEVICE. */
+size_t w4a8_paged_attention_workspace_size(const w4a8_kv_view* view, int q_heads, int max_q,
+                                           int max_len);
+w4a8_status w4a8_paged_attention(const uint16_t* q_dev, int ldq, int q_heads,
+                                 const w4a8_kv_view* view, int max_q, int max_len, float scale,
+                                 int window, uint16_t* out_dev, int ldo, void* workspace_dev,
+                                 size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------- measurement aid
  * Not part of the layer.  A read-only stream over `bytes` of device memory
  * (16-byte aligned, a multiple of 16) by `workgroups` x 512 threads, with

@@ -58,30 +58,46 @@ def rotate(x, pos, cos_sin, interleaved):
 
 
 def attention(q, cache, scale_kv, table, lens, cu, scale, window=0):
-    """o [tokens, heads, dim] float64 over a paged int8 cache.  Row by row;
-    a row that sees no key is 0."""
+    """(o, bound) [tokens, heads, dim] float64 over a paged int8 cache, row by
+    row; a row that sees no key is 0, pages outside the pool are not seen.
+
+    bound is what the kernels' arithmetic may add to o: half an fp16 ulp of
+    the result; softmax weights rounded to fp16 (2^-11 of each, so of
+    sum p |v|); and scores summed in fp32, whose error d (dim + 8 roundings
+    of sum |q||k| * scale) changes each weight and their sum by at most
+    exp(2d) - 1."""
     tokens, heads, dim = q.shape
     pages, _, kv_heads, page, _ = cache.shape
     group = heads // kv_heads
     out = np.zeros((tokens, heads, dim))
+    bound = np.full((tokens, heads, dim), half_ulp16(0))
     for b in range(len(lens)):
         n = cu[b + 1] - cu[b]
         length = int(lens[b])
-        ids = [int(table[b, i]) for i in range(-(-length // page))]
+        ids = np.array([int(table[b, i]) for i in range(-(-length // page))], dtype=np.int64)
+        there = np.repeat((ids >= 0) & (ids < pages), page)[:length]
+        ids = np.where((ids >= 0) & (ids < pages), ids, 0)
         for h in range(kv_heads):
-            if not ids:
+            if not len(ids):
                 continue
-            k = np.concatenate([cache[p, 0, h].astype(np.float64) * float(scale_kv[p, 0, h])
-                                for p in ids])[:length]
-            v = np.concatenate([cache[p, 1, h].astype(np.float64) * float(scale_kv[p, 1, h])
-                                for p in ids])[:length]
+            code = cache[ids][:, :, h].astype(np.float64) * scale_kv[ids][:, :, h].astype(np.float64)[..., None, None]
+            k, v = code[:, 0].reshape(-1, dim)[:length], code[:, 1].reshape(-1, dim)[:length]
             for i in range(n):
                 pos = length - n + i
                 lo = max(0, pos - window + 1) if window else 0
                 if pos < 0:
                     continue
+                see = np.arange(lo, pos + 1)
+                see = see[there[lo:pos + 1]]
+                if not len(see):
+                    continue
                 rows = q[cu[b] + i, h * group:(h + 1) * group].astype(np.float64)
-                x = rows @ k[lo:pos + 1].T * scale
-                x = np.exp(x - x.max(axis=1, keepdims=True))
-                out[cu[b] + i, h * group:(h + 1) * group] = (x / x.sum(axis=1, keepdims=True)) @ v[lo:pos + 1]
-    return out
+                x = rows @ k[see].T * scale
+                p = np.exp(x - x.max(axis=1, keepdims=True))
+                p /= p.sum(axis=1, keepdims=True)
+                o = p @ v[see]
+                d = (np.abs(rows) @ np.abs(k[see]).T).max(axis=1, keepdims=True) * abs(scale) * (dim + 8) * 2.0 ** -24
+                at = cu[b] + i, slice(h * group, (h + 1) * group)
+                out[at] = o
+                bound[at] = half_ulp16(np.abs(o)) * 1.001 + (p @ np.abs(v[see])) * (2.0 ** -11 + np.expm1(2 * d) + 2.0 ** -19)
+    return out, bound

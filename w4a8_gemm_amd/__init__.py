@@ -52,6 +52,16 @@ class GemmOpts(ctypes.Structure):
                 ("slices", ctypes.c_int), ("workgroups", ctypes.c_int)]
 
 
+class KvView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("page_stride", ctypes.c_longlong), ("scale_stride", ctypes.c_longlong),
+                ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("block_table", ctypes.c_void_p), ("block_table_ld", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("seq_lens", ctypes.c_void_p),
+                ("cu_q", ctypes.c_void_p), ("batch", ctypes.c_int), ("total_q", ctypes.c_int)]
+
+
 def _load():
     # torch is imported first on purpose: it carries its own HIP runtime
     # (same soname as the system one).  Loading it first makes the library's
@@ -81,6 +91,9 @@ def _load():
         "w4a8_read_probe": (I, [P, Z, I, P, P]),
         "w4a8_rms_norm_quant": (I, [P, I, P, I, P, ctypes.c_float, I, I, P, I, P, I, P, P]),
         "w4a8_silu_mul_quant": (I, [P, I, P, I, I, I, P, I, P, P]),
+        "w4a8_rope_append": (I, [P, I, P, I, P, I, I, P, I, I, I, P, P, I, P]),
+        "w4a8_paged_attention_workspace_size": (Z, [P, I, I, I]),
+        "w4a8_paged_attention": (I, [P, I, I, P, I, I, ctypes.c_float, I, P, I, P, Z, P]),
         "w4a8_gemm_noalloc": (I, [P, I, P, I, P, I, I, I, P, I, P, I, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -380,6 +393,158 @@ def silu_mul_quant(gate, up=None, a8=None, s_a=None, stream=None):
                                    _ld(a8), s_a.data_ptr(), _stream_ptr(stream)),
            "w4a8_silu_mul_quant")
     return a8, s_a
+
+
+def kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device="cuda"):
+    """A paged int8 KV cache: (cache int8 [num_pages, 2, kv_heads, page_size,
+    head_dim], scale float16 [num_pages, 2, kv_heads]), [:, 0] the keys."""
+    torch = _torch()
+    return (torch.zeros((num_pages, 2, kv_heads, page_size, head_dim), dtype=torch.int8, device=device),
+            torch.zeros((num_pages, 2, kv_heads), dtype=torch.float16, device=device))
+
+
+def rope_table(max_pos: int, rotary_dim: int, base: float = 10000.0, scaling: str | None = None,
+               factor: float = 1.0, original_max_pos: int = 8192, low: float = 1.0,
+               high: float = 4.0, device="cuda"):
+    """cos_sin for rope_append(): float32 [max_pos, rotary_dim], cosines then
+    sines, computed in 64 bits from the frequencies base^(-2i / rotary_dim).
+
+    scaling  None
+             "linear": every frequency / factor
+             "base":   base * factor^(rotary_dim / (rotary_dim - 2)), which
+                       leaves the highest frequency and divides the lowest by
+                       factor
+             "bands":  frequencies that turn fewer than `low` times within
+                       original_max_pos / factor, those that turn more than
+                       `high` times kept, a linear blend between (the scheme
+                       of Llama-3.1's checkpoints)
+    """
+    torch = _torch()
+    if max_pos < 1 or rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rope_table: max_pos >= 1 and an even rotary_dim >= 2 are needed")
+    if factor <= 0 or base <= 0 or (scaling == "bands" and not 0 < low < high):
+        raise ValueError("rope_table: factor and base must be positive, and 0 < low < high")
+    exponent = torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim
+    if scaling == "base" and rotary_dim > 2:
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    freq = base ** -exponent
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "bands":
+        turns = original_max_pos * freq / (2 * np.pi)
+        keep = ((turns - low) / (high - low)).clamp(0, 1)
+        freq = freq * keep + freq / factor * (1 - keep)
+    elif scaling not in (None, "base"):
+        raise ValueError(f"rope_table: unknown scaling {scaling!r}")
+    angle = torch.arange(max_pos, dtype=torch.float64)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], dim=1).float().to(device)
+
+
+def _kv_view(cache, scale, block_table, seq_lens, cu_q, total_q):
+    """The C view of a cache and a batch, its tensors checked."""
+    torch = _torch()
+    if cache.dtype is not torch.int8 or cache.dim() != 5 or cache.shape[1] != 2 or not cache.is_cuda:
+        raise ValueError("cache: expected an int8 CUDA tensor [pages, 2, kv_heads, page_size, head_dim]")
+    pages, _, heads, page, dim = cache.shape
+    if cache.stride()[1:] != (heads * page * dim, page * dim, dim, 1):
+        raise ValueError("cache: the values of a page must be contiguous")
+    if scale.dtype is not torch.float16 or scale.shape != (pages, 2, heads) or not scale.is_cuda \
+            or scale.stride()[1:] != (heads, 1):
+        raise ValueError(f"scale: expected a float16 CUDA tensor [{pages}, 2, {heads}], "
+                         "contiguous within a page")
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or not block_table.is_cuda \
+            or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+        raise ValueError("block_table: expected an int32 CUDA tensor [batch, pages of a sequence]")
+    batch, max_pages = block_table.shape
+    if seq_lens.dtype is not torch.int32 or seq_lens.shape != (batch,) or not seq_lens.is_cuda \
+            or not seq_lens.is_contiguous():
+        raise ValueError(f"seq_lens: expected a contiguous int32 CUDA tensor of {batch} values")
+    if cu_q is not None and (cu_q.dtype is not torch.int32 or cu_q.shape != (batch + 1,)
+                             or not cu_q.is_cuda or not cu_q.is_contiguous()):
+        raise ValueError(f"cu_q: expected a contiguous int32 CUDA tensor of {batch + 1} values")
+    if cu_q is None and total_q != batch:
+        raise ValueError(f"without cu_q each of the {batch} sequences brings one token, got {total_q}")
+    return KvView(cache.data_ptr(), scale.data_ptr(),
+                  cache.stride(0) if pages > 1 else 2 * heads * page * dim,
+                  scale.stride(0) if pages > 1 else 2 * heads, pages, page, heads, dim,
+                  block_table.data_ptr(),
+                  block_table.stride(0) if batch > 1 else max(block_table.stride(0), max_pages),
+                  max_pages, seq_lens.data_ptr(), cu_q.data_ptr() if cu_q is not None else None,
+                  batch, total_q)
+
+
+def _heads(name, t, tokens=None, heads=None, dim=None):
+    """Check a [tokens, heads, dim] float16 CUDA tensor whose rows (all heads of
+    a token) are contiguous; returns the row stride."""
+    torch = _torch()
+    if t.dtype is not torch.float16 or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name}: expected a float16 CUDA tensor [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    if (tokens is not None and n != tokens) or (heads is not None and h != heads) \
+            or (dim is not None and d != dim):
+        raise ValueError(f"{name}: expected shape ({tokens}, {heads or 'heads'}, {dim}), got {tuple(t.shape)}")
+    s = t.stride()
+    if s[2] != 1 or (h > 1 and s[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s[0] if n > 1 else max(s[0], h * d)
+
+
+def rope_append(q, k, v, cos_sin, cache, scale, block_table, seq_lens, cu_q=None,
+                interleaved: bool = False, out=None, stream=None):
+    """Rotate q [tokens, heads, dim] and k by position and append k and v
+    [tokens, kv_heads, dim] to the paged cache; returns the rotated q (a new
+    tensor, or `out`, which may be q).  cos_sin [max_pos, rotary_dim] is
+    rope_table()'s, or None for no rotation.  See w4a8_rope_append."""
+    torch = _torch()
+    tokens, heads, dim = q.shape
+    view = _kv_view(cache, scale, block_table, seq_lens, cu_q, tokens)
+    ldq = _heads("q", q, tokens, None, view.head_dim)
+    ldk = _heads("k", k, tokens, view.kv_heads, view.head_dim)
+    ldv = _heads("v", v, tokens, view.kv_heads, view.head_dim)
+    rotary = max_pos = 0
+    if cos_sin is not None:
+        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_cuda \
+                or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin: expected a contiguous float32 CUDA tensor [max_pos, rotary_dim]")
+        max_pos, rotary = cos_sin.shape
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=torch.float16, device=q.device)
+    _check(lib.w4a8_rope_append(
+        q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, heads,
+        cos_sin.data_ptr() if cos_sin is not None else None, rotary, max_pos, int(interleaved),
+        ctypes.byref(view), out.data_ptr(), _heads("out", out, tokens, heads, dim),
+        _stream_ptr(stream)), "w4a8_rope_append")
+    return out
+
+
+def paged_attention(q, cache, scale_kv, block_table, seq_lens, cu_q=None, max_q: int | None = None,
+                    max_len: int | None = None, scale: float | None = None, window: int = 0, out=None, workspace=None,
+                    stream=None):
+    """Causal attention of q [tokens, heads, dim] over the paged int8 cache;
+    returns o like q.  max_q and max_len bound the new tokens of a sequence
+    and seq_lens on the host (defaults: all of q, and what the block table
+    holds); scale defaults to dim ** -0.5.  See w4a8_paged_attention."""
+    torch = _torch()
+    tokens, heads, dim = q.shape
+    view = _kv_view(cache, scale_kv, block_table, seq_lens, cu_q, tokens)
+    ldq = _heads("q", q, tokens, None, view.head_dim)
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=torch.float16, device=q.device)
+    if max_len is None:
+        max_len = view.max_pages * view.page_size
+    if max_q is None:
+        max_q = 1 if cu_q is None else tokens
+    need = lib.w4a8_paged_attention_workspace_size(ctypes.byref(view), heads, max_q, max_len)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check(lib.w4a8_paged_attention(
+        q.data_ptr(), ldq, heads, ctypes.byref(view), max_q, max_len,
+        dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+        _heads("out", out, tokens, heads, dim),
+        workspace.data_ptr() if workspace is not None else None,
+        workspace.numel() * workspace.element_size() if workspace is not None else 0,
+        _stream_ptr(stream)), "w4a8_paged_attention")
+    return out
 
 
 def read_probe(buf, offset: int, nbytes: int, workgroups: int, sink, stream=None):

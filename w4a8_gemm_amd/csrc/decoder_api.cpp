@@ -10,6 +10,174 @@
 
 using namespace w4a8;
 
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// rows of `cols` fp16 values read and written 16 bytes at a time
+bool rows_ok(const void* p, int ld, long cols) {
+  return p && aligned16(p) && ld >= cols && ld % 8 == 0;
+}
+
+// The view's sizes and pointers; on success fills `a`.  A view of an empty
+// batch or of no new tokens is accepted with null pointers (`a` is then
+// not used).
+w4a8_status check_view(const w4a8_kv_view* v, KvArgs* a) {
+  if (!v) return W4A8_ERR_INVALID_ARGUMENT;
+  if (v->num_pages < 1 || v->kv_heads < 1 || v->batch < 0 || v->total_q < 0 || v->max_pages < 1 ||
+      v->block_table_ld < v->max_pages || v->batch > W4A8_M_MAX || v->total_q > W4A8_M_MAX)
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (v->head_dim < 16 || v->head_dim > W4A8_HEAD_DIM_MAX || v->head_dim % 16 ||
+      v->kv_heads > W4A8_HEADS_MAX)
+    return W4A8_ERR_UNSUPPORTED;
+  int shift = 4;
+  while (shift < 10 && (1 << shift) < v->page_size) ++shift;
+  if (v->page_size != 1 << shift) return W4A8_ERR_UNSUPPORTED;
+  if (long(v->max_pages) << shift > 2147483647l - v->page_size) return W4A8_ERR_INVALID_ARGUMENT;
+  // without cu_q every sequence brings one token
+  if (!v->cu_q_dev && v->total_q != v->batch) return W4A8_ERR_INVALID_ARGUMENT;
+  const long block = long(v->page_size) * v->head_dim;
+  const long page = 2l * v->kv_heads * block;
+  if (v->page_stride < page || v->page_stride % 16 || v->scale_stride < 2l * v->kv_heads)
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (v->batch == 0 || v->total_q == 0) return W4A8_OK;
+  if (!v->data_dev || !v->scale_dev || !v->block_table_dev || !v->seq_lens_dev)
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (!aligned16(v->data_dev)) return W4A8_ERR_INVALID_ARGUMENT;
+  a->data = v->data_dev;
+  a->scale = v->scale_dev;
+  a->page_stride = long(v->page_stride);
+  a->scale_stride = long(v->scale_stride);
+  a->num_pages = v->num_pages;
+  a->kv_heads = v->kv_heads;
+  a->dim = v->head_dim;
+  a->page_shift = shift;
+  a->table = v->block_table_dev;
+  a->table_ld = v->block_table_ld;
+  a->max_pages = v->max_pages;
+  a->lens = v->seq_lens_dev;
+  a->cu_q = v->cu_q_dev;
+  a->batch = v->batch;
+  a->total_q = v->total_q;
+  return W4A8_OK;
+}
+
+// What the attention launches for a batch.
+struct AttnPlan {
+  int splits;
+  size_t workspace;
+};
+
+// Keys are split over workgroups until about kTargetWgs run (two per compute
+// unit), each split keeping at least kMinKeys keys of the longest sequence.
+constexpr long kTargetWgs = 512;
+constexpr int kMinKeys = 256;
+constexpr int kMaxSplits = 64;
+
+AttnPlan plan_attn(const KvArgs& kv, int q_heads, int max_q, int max_len) {
+  (void)max_q;
+  AttnPlan pl;
+  const int group = q_heads / kv.kv_heads;
+  const long wgs = attn_tiles(kv, group, kAttnRows) * kv.kv_heads;
+  long splits = (kTargetWgs + wgs - 1) / wgs;
+  const long most = max_len / kMinKeys;
+  if (splits > most) splits = most;
+  if (splits > kMaxSplits) splits = kMaxSplits;
+  if (splits < 1) splits = 1;
+  pl.splits = int(splits);
+  pl.workspace = splits > 1 ? size_t(kv.total_q) * size_t(q_heads) * size_t(splits) *
+                                  size_t(kv.dim + 2) * 4u
+                            : 0;
+  return pl;
+}
+
+w4a8_status check_heads(const KvArgs& kv, int q_heads) {
+  if (q_heads < 1) return W4A8_ERR_INVALID_ARGUMENT;
+  if (q_heads % kv.kv_heads || q_heads > W4A8_HEADS_MAX) return W4A8_ERR_UNSUPPORTED;
+  if (long(kv.total_q) * q_heads > 2147483647l) return W4A8_ERR_UNSUPPORTED;
+  return W4A8_OK;
+}
+
+}  // namespace
+
+extern "C" w4a8_status w4a8_rope_append(const uint16_t* q_dev, int ldq, const uint16_t* k_dev,
+                                        int ldk, const uint16_t* v_dev, int ldv, int q_heads,
+                                        const float* cos_sin_dev, int rotary_dim, int max_pos,
+                                        int interleaved, const w4a8_kv_view* view,
+                                        uint16_t* q_out_dev, int ldqo, void* stream) {
+  AppendParams p;
+  w4a8_status st = check_view(view, &p.kv);
+  if (st != W4A8_OK) return st;
+  if (rotary_dim < 0 || rotary_dim > view->head_dim || (rotary_dim > 0 && max_pos < 1))
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (rotary_dim % 16) return W4A8_ERR_UNSUPPORTED;
+  if (q_heads < 1) return W4A8_ERR_INVALID_ARGUMENT;
+  if (q_heads > W4A8_HEADS_MAX) return W4A8_ERR_UNSUPPORTED;
+  if (view->batch == 0 || view->total_q == 0) return W4A8_OK;
+  const long q_cols = long(q_heads) * p.kv.dim, kv_cols = long(p.kv.kv_heads) * p.kv.dim;
+  if (!rows_ok(q_dev, ldq, q_cols) || !rows_ok(k_dev, ldk, kv_cols) ||
+      !rows_ok(v_dev, ldv, kv_cols) || !rows_ok(q_out_dev, ldqo, q_cols))
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (rotary_dim > 0 && (!cos_sin_dev || !aligned16(cos_sin_dev))) return W4A8_ERR_INVALID_ARGUMENT;
+  p.q = q_dev;
+  p.k = k_dev;
+  p.v = v_dev;
+  p.q_out = q_out_dev;
+  p.ldq = ldq;
+  p.ldk = ldk;
+  p.ldv = ldv;
+  p.ldqo = ldqo;
+  p.q_heads = q_heads;
+  p.cos_sin = cos_sin_dev;
+  p.rotary = rotary_dim;
+  p.max_pos = max_pos;
+  p.interleaved = interleaved;
+  return device_status(launch_rope_append(p, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" size_t w4a8_paged_attention_workspace_size(const w4a8_kv_view* view, int q_heads,
+                                                      int max_q, int max_len) {
+  KvArgs kv;
+  if (check_view(view, &kv) != W4A8_OK || view->batch == 0 || view->total_q == 0) return 0;
+  if (check_heads(kv, q_heads) != W4A8_OK || max_q < 0 || max_len < 0) return 0;
+  return plan_attn(kv, q_heads, max_q, max_len).workspace;
+}
+
+extern "C" w4a8_status w4a8_paged_attention(const uint16_t* q_dev, int ldq, int q_heads,
+                                            const w4a8_kv_view* view, int max_q, int max_len,
+                                            float scale, int window, uint16_t* out_dev, int ldo,
+                                            void* workspace_dev, size_t workspace_bytes,
+                                            void* stream) {
+  AttnParams p;
+  w4a8_status st = check_view(view, &p.kv);
+  if (st != W4A8_OK) return st;
+  if (max_q < 0 || max_len < 0 || window < 0 || !std::isfinite(scale)) return W4A8_ERR_INVALID_ARGUMENT;
+  if (view->batch == 0 || view->total_q == 0) return W4A8_OK;
+  st = check_heads(p.kv, q_heads);
+  if (st != W4A8_OK) return st;
+  const long cols = long(q_heads) * p.kv.dim;
+  if (!rows_ok(q_dev, ldq, cols) || !rows_ok(out_dev, ldo, cols)) return W4A8_ERR_INVALID_ARGUMENT;
+  const AttnPlan pl = plan_attn(p.kv, q_heads, max_q, max_len);
+  if (pl.workspace > 0) {
+    if (workspace_bytes < pl.workspace) return W4A8_ERR_BUFFER_TOO_SMALL;
+    if (!workspace_dev || !aligned16(workspace_dev)) return W4A8_ERR_INVALID_ARGUMENT;
+  }
+  p.q = q_dev;
+  p.out = out_dev;
+  p.ldq = ldq;
+  p.ldo = ldo;
+  p.q_heads = q_heads;
+  p.group = q_heads / p.kv.kv_heads;
+  p.scale_log2e = scale * 1.44269504f;
+  p.window = window;
+  p.splits = pl.splits;
+  p.part = static_cast<float*>(workspace_dev);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  st = device_status(launch_paged_attn(p, s));
+  if (st != W4A8_OK || pl.splits == 1) return st;
+  return device_status(launch_attn_join(p, s));
+}
+
 extern "C" w4a8_status w4a8_rms_norm_quant(const uint16_t* x_dev, int ldx,
                                            const uint16_t* residual_dev, int ldr,
                                            const uint16_t* weight_dev, float eps, int m, int k,

@@ -39,6 +39,66 @@ struct SwigluParams {
 hipError_t launch_rms_norm_quant(const NormParams& p, hipStream_t stream);
 hipError_t launch_silu_mul_quant(const SwigluParams& p, hipStream_t stream);
 
+// The paged cache and the batch that one call reads or writes (the C ABI's
+// w4a8_kv_view, validated), as the kernels take it.
+struct KvArgs {
+  int8_t* data;               // [num_pages][2][kv_heads][page][dim], pages page_stride apart
+  uint16_t* scale;            // [num_pages][2][kv_heads], pages scale_stride apart
+  long page_stride, scale_stride;
+  int num_pages, kv_heads, dim;
+  int page_shift;             // page size = 1 << page_shift
+  const int32_t* table;
+  int table_ld, max_pages;
+  const int32_t* lens;
+  const int32_t* cu_q;        // null: one new token per sequence
+  int batch, total_q;
+};
+
+struct AppendParams {
+  KvArgs kv;
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* q_out;
+  int ldq, ldk, ldv, ldqo;
+  int q_heads;
+  const float* cos_sin;       // [max_pos][rotary]: cosines, then sines
+  int rotary, max_pos;
+  int interleaved;
+};
+
+// Virtual page slots of an append: sequence b's written pages have the
+// indices floor(cu_q[b] / page) + 2b ... (a sequence of n tokens touches at
+// most floor(n / page) + 2 pages wherever it starts, so the ranges are
+// disjoint); one slot per sequence where each brings one token.
+inline long append_slots(const KvArgs& kv) {
+  return kv.cu_q ? (long(kv.total_q) >> kv.page_shift) + 2l * kv.batch : long(kv.batch);
+}
+hipError_t launch_rope_append(const AppendParams& p, hipStream_t stream);
+
+struct AttnParams {
+  KvArgs kv;
+  const uint16_t* q;
+  uint16_t* out;
+  int ldq, ldo;
+  int q_heads, group;         // group = q_heads / kv_heads
+  float scale_log2e;          // score scale * log2(e)
+  int window;                 // 0: none
+  int splits;                 // workgroups that split one row tile's keys
+  float* part;                // splits > 1: partial results, see paged_attn.hip
+};
+
+// Row tiles of the attention: the rows of a sequence and kv head are its
+// (token, query head of the group) pairs, tiled by `rows`; sequence b's
+// tiles have the indices floor(cu_q[b] * group / rows) + b ...
+inline long attn_tiles(const KvArgs& kv, int group, int rows) {
+  return kv.cu_q ? long(kv.total_q) * group / rows + kv.batch
+                 : long(kv.batch) * ((group + rows - 1) / rows);
+}
+constexpr int kAttnRows = 16;   // rows of a tile (paged_attn.hip)
+hipError_t launch_paged_attn(const AttnParams& p, hipStream_t stream);
+hipError_t launch_attn_join(const AttnParams& p, hipStream_t stream);
+
 // Turns a HIP status into the C ABI's and keeps it for
 // w4a8_last_device_error (api.cpp).
 w4a8_status device_status(hipError_t e);

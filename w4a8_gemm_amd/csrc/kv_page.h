@@ -1,0 +1,61 @@
+// Device helpers shared by the append and the attention over the paged int8
+// cache: which sequence a virtual index belongs to, and where a page lies.
+//
+// Everything read from device memory (lengths, offsets, page numbers) is
+// clamped to the bounds the host checked, so that no content of those tables
+// can take a kernel outside its buffers.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "decoder_kernels.h"
+
+namespace w4a8 {
+namespace kv {
+
+// A sequence's new tokens [lo, hi) among all new tokens, and its length with
+// them.  The position of new token t is len - (hi - lo) + (t - lo).
+struct Seq {
+  int lo, hi, len;
+};
+
+static __device__ __forceinline__ Seq seq_of(const KvArgs& a, int b) {
+  Seq s;
+  if (a.cu_q) {
+    s.lo = min(max(a.cu_q[b], 0), a.total_q);
+    s.hi = min(max(a.cu_q[b + 1], s.lo), a.total_q);
+  } else {
+    s.lo = b;
+    s.hi = b + 1;
+  }
+  // max_pages << page_shift fits an int (host check)
+  s.len = min(max(a.lens[b], 0), a.max_pages << a.page_shift);
+  return s;
+}
+
+// The largest b with first(b) <= w, first(b) = floor(cu_q[b] * mul >> / div)
+// + per * b: the sequence that owns virtual index w; *index is w's place in it.
+// first(0) is 0 for a proper cu_q; an improper one gives some sequence in range.
+template <typename First>
+static __device__ __forceinline__ int owner(int w, int batch, First first, int* index) {
+  int lo = 0, hi = batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first(mid) <= w)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  *index = w - first(lo);
+  return lo;
+}
+
+// page number `i` of sequence b, or -1 where the table holds none
+static __device__ __forceinline__ int page_at(const KvArgs& a, int b, int i) {
+  if (i < 0 || i >= a.max_pages) return -1;
+  const int p = a.table[long(b) * a.table_ld + i];
+  return p >= 0 && p < a.num_pages ? p : -1;
+}
+
+}  // namespace kv
+}  // namespace w4a8
