@@ -47,7 +47,8 @@ def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     steps = []
     for src in ("fused.hip", "skinny.hip", "tiled.hip", "quant_act.hip", "w4a16.hip",
-                "probe.hip", "scratch.hip", "row_quant.hip", "kv_append.hip", "paged_attn.hip"):
+                "probe.hip", "scratch.hip", "row_quant.hip", "kv_append.hip", "paged_attn.hip",
+                "paged_attn_tile.hip"):
         obj = os.path.join(BUILD, src + ".o")
         steps.append((obj, [HIPCC, *HIP_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]))
     for src in ("api.cpp", "configs.cpp", "decoder_api.cpp"):

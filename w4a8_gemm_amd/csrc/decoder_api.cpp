@@ -62,8 +62,11 @@ w4a8_status check_view(const w4a8_kv_view* v, KvArgs* a) {
   return W4A8_OK;
 }
 
-// What the attention launches for a batch.
+// What the attention launches for a batch: the kernel of 16-row tiles
+// (waves == 0) or the one of 32 rows a wave, and how many workgroups split
+// the keys of a row tile.
 struct AttnPlan {
+  int waves;
   int splits;
   size_t workspace;
 };
@@ -75,10 +78,13 @@ constexpr int kMinKeys = 256;
 constexpr int kMaxSplits = 64;
 
 AttnPlan plan_attn(const KvArgs& kv, int q_heads, int max_q, int max_len) {
-  (void)max_q;
   AttnPlan pl;
   const int group = q_heads / kv.kv_heads;
-  const long wgs = attn_tiles(kv, group, kAttnRows) * kv.kv_heads;
+  const long rows = long(kv.cu_q ? max_q : 1) * group;
+  pl.waves = 0;
+  if (rows > kAttnRows) pl.waves = kv.dim > 64 && kv.dim <= 128 && rows > 128 ? 8 : 4;
+  const int tile = pl.waves ? 32 * pl.waves : kAttnRows;
+  const long wgs = attn_tiles(kv, group, tile) * kv.kv_heads;
   long splits = (kTargetWgs + wgs - 1) / wgs;
   const long most = max_len / kMinKeys;
   if (splits > most) splits = most;
@@ -173,7 +179,7 @@ extern "C" w4a8_status w4a8_paged_attention(const uint16_t* q_dev, int ldq, int 
   p.splits = pl.splits;
   p.part = static_cast<float*>(workspace_dev);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  st = device_status(launch_paged_attn(p, s));
+  st = device_status(pl.waves ? launch_paged_attn_tile(p, pl.waves, s) : launch_paged_attn(p, s));
   if (st != W4A8_OK || pl.splits == 1) return st;
   return device_status(launch_attn_join(p, s));
 }

@@ -97,6 +97,8 @@ inline long attn_tiles(const KvArgs& kv, int group, int rows) {
 }
 constexpr int kAttnRows = 16;   // rows of a tile (paged_attn.hip)
 hipError_t launch_paged_attn(const AttnParams& p, hipStream_t stream);
+// 32 rows a wave, 4 waves, or 8 where 64 < dim <= 128 (paged_attn_tile.hip)
+hipError_t launch_paged_attn_tile(const AttnParams& p, int waves, hipStream_t stream);
 hipError_t launch_attn_join(const AttnParams& p, hipStream_t stream);
 
 // Turns a HIP status into the C ABI's and keeps it for
