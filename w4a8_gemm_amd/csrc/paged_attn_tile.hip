@@ -19,10 +19,13 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "attn_common.h"
 #include "decoder_kernels.h"
 #include "kv_page.h"
 #include "quant_common.h"
+#include "tile_common.h"
 
 namespace w4a8 {
 namespace {
@@ -30,10 +33,8 @@ namespace {
 using namespace attn;
 using namespace dev;
 
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-constexpr int kKeys = 64;     // keys of a tile
-constexpr int kGroups = kKeys / 16;
 
 // Weights above 2^kRoom make a row move its maximum (fp16 ends at 2^16).
 constexpr float kRoom = 15.0f;
@@ -54,36 +55,62 @@ __device__ __forceinline__ float pair_sum(float x) {
   return __builtin_bit_cast(float, uint32_t(s[0])) + __builtin_bit_cast(float, uint32_t(s[1]));
 }
 
-// LDS places, in 16-byte chunks of 8 halves.  A column of chunks is read by
-// 32 lanes of consecutive rows; the row-dependent exclusive or spreads 8
-// neighbouring rows over all banks (and, for values, the 4-row steps of
-// the transposing writes).
+// LDS places, in bytes.  Rows of keys hold DP halves, rows of V^T (one per
+// column d) KEYS halves, in 16-byte chunks.  A column of chunks is read by 32
+// lanes of consecutive rows, so the row number is spread over the banks by an
+// exclusive or on the chunk number: 8 neighbouring rows take all banks, and so
+// do, for V^T, the 4-row steps of the transposing writes.
 template <int DP>
-__device__ __forceinline__ int k_chunk(int key, int c) {
-  return key * (DP / 8) + (c ^ (key & (DP / 8 - 1) & 15));
+__device__ __forceinline__ int k_place(int key, int c) {
+  return key * (DP * 2) + ((c ^ (key & (DP / 8 - 1) & 15)) << 4);
 }
-__device__ __forceinline__ int v_chunk(int d, int c) {
-  return d * (kKeys / 8) + (c ^ ((d ^ (d >> 3)) & 7));
+template <int KEYS>
+__device__ __forceinline__ int v_place(int d, int c) {
+  const int f = KEYS == 64 ? (d ^ (d >> 3)) & 7 : ((d >> 1) ^ (d >> 3)) & 3;
+  return d * (KEYS * 2) + ((c ^ f) << 4);
 }
 
 struct GroupScale {   // of 16 keys
   float sk, lv, rv, pad;
 };
 
-template <int DP, bool PAD, int NW>
-__global__ __launch_bounds__(64 * NW, DP == 128 ? 2 : 1) void attn_tile_kernel(AttnParams p) {
+// uniform 4-byte load through the scalar path
+__device__ __forceinline__ int scalar_load(const int32_t* p) {
+  return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t(p));
+}
+
+// Barrier of the workgroup that makes LDS writes visible and, unlike
+// __syncthreads, leaves loads from memory in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// DP: head dim rounded up to 64, 128 or 256 (PAD: dim < DP); NW waves; SUB
+// 32-key subtiles per staged tile.
+template <int DP, bool PAD, int NW, int SUB>
+__global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(AttnParams p) {
   constexpr int kThreads = 64 * NW;
   constexpr int kRows = 32 * NW;
-  constexpr int kSteps = DP / 16;                       // products of a score tile
+  constexpr int kKeys = 32 * SUB;
+  constexpr int kGroups = kKeys / 16;
+  constexpr int kSteps = DP / 16;                       // products of a score subtile
   constexpr int kDTiles = DP / 32;
   constexpr int kUnits = kKeys * DP / 16 / kThreads;    // 16-code units of a thread, K and V each
+  constexpr int kWaveKeys = 1024 / DP;                  // keys of a wave's unit: within 16 aligned ones
+  constexpr int kUnitKeys = kThreads * 16 / DP;         // keys from one unit of a thread to the next
   static_assert(kUnits * kThreads * 16 == kKeys * DP, "units divide evenly");
+  static_assert(kUnits == 1 || kUnitKeys % 16 == 0, "the swizzles repeat from unit to unit");
   const KvArgs& kv = p.kv;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r32 = lane & 31, h = lane >> 5;
 
-  __shared__ half8_t sh_k[2][kKeys * DP / 8];
-  __shared__ half8_t sh_v[2][DP * kKeys / 8];
+  // two tiles deep: see the loop
+  constexpr int kTileBytes = kKeys * DP * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t sh_k[2 * kTileBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sh_v[2 * kTileBytes];
   __shared__ GroupScale sh_s[2][kGroups];
 
   // heads fastest (neighbouring workgroups land on different dies, so a die
@@ -114,22 +141,26 @@ __global__ __launch_bounds__(64 * NW, DP == 128 ? 2 : 1) void attn_tile_kernel(A
   // keys the row sees
   const int see_hi = row_ok ? start + t + 1 : 0;
   const int see_lo = p.window > 0 ? max(start + t - p.window + 1, 0) : 0;
-  // keys the workgroup's rows see, and the wave's
+  // keys that some row of the workgroup sees, that some row of the wave sees,
+  // that all 32 see
   const int wg_t0 = nth * kRows / p.group, wg_t1 = (min(rows, (nth + 1) * kRows) - 1) / p.group;
   const int all_hi = max(start + wg_t1 + 1, 0);
   const int all_lo = p.window > 0 ? max(start + wg_t0 - p.window + 1, 0) : 0;
   const int w_row0 = min(nth * kRows + wave * 32, rows), w_row1 = min(w_row0 + 32, rows);
   const bool w_any = w_row0 < w_row1;
   const int w_t0 = w_any ? w_row0 / p.group : 0, w_t1 = w_any ? (w_row1 - 1) / p.group : 0;
-  const int w_hi = w_any ? start + w_t1 + 1 : 0;                          // some row sees below this
+  const int w_hi = w_any ? start + w_t1 + 1 : 0;
   const int w_lo = p.window > 0 ? max(start + w_t0 - p.window + 1, 0) : 0;
-  const int w_all_hi = w_any && w_row1 - w_row0 == 32 ? start + w_t0 + 1 : 0;   // every row does
+  const int w_all_hi = w_row1 - w_row0 == 32 ? start + w_t0 + 1 : 0;
   const int w_all_lo = p.window > 0 ? max(start + w_t1 - p.window + 1, 0) : 0;
 
   const int tile0 = all_lo / kKeys;
   const int n_tiles = max((all_hi + kKeys - 1) / kKeys - tile0, 0);
   const int first = tile0 + int(long(n_tiles) * split / p.splits);
   const int last = tile0 + int(long(n_tiles) * (split + 1) / p.splits);
+  // the tiles among them that some row of the wave sees
+  const int w_first = max(first, w_lo / kKeys);
+  const int w_last = min(last, (w_hi + kKeys - 1) / kKeys);
 
   // Q^T: the lane's row, d = 16 i + 8 h ..; a negative score scale turns
   // the queries instead, so that the factors of the scores are >= 0
@@ -151,88 +182,113 @@ __global__ __launch_bounds__(64 * NW, DP == 128 ? 2 : 1) void attn_tile_kernel(A
   const float factor = fabsf(p.scale_log2e) * kCodeScale;
 
   // A thread's units.  Keys: unit = (key, 16 codes of it).  Values: 4 keys
-  // x 4 columns.
+  // x 4 columns.  A wave's share of a tile lies in one page, so its address
+  // is scalar up to a fixed offset of the lane.
   const long head_bytes = long(kv.dim) << kv.page_shift;
   const int slot_mask = (1 << kv.page_shift) - 1;
-  uint4 kreg[kUnits], vreg[kUnits];
-  int kpage[kUnits], vpage[kUnits];
-  int gpage = -1, gthere = -1;           // threads below kGroups: a group's page
-  uint16_t gsk = 0, gsv = 0;             // and its scales
+  const int8_t* const k_base = kv.data + head * head_bytes;
+  const int8_t* const v_base = k_base + kv.kv_heads * head_bytes;
+  const int k_lane_key = lane / (DP / 16), k_lane_d = lane % (DP / 16) * 16;
+  const int v_lane_key = lane / (DP / 4) * 4, v_lane_d = lane % (DP / 4) * 4;
+  const unsigned k_off = unsigned(k_lane_key * kv.dim + k_lane_d);
+  const unsigned v_off = unsigned(v_lane_key * kv.dim + v_lane_d);
+  const bool k_there = !PAD || k_lane_d < kv.dim, v_there = !PAD || v_lane_d < kv.dim;
+  u32x4 kreg[kUnits], vreg[kUnits];
+  int kpage[kUnits], vpage[kUnits];      // of the next tiles to load
+  int gpage = -1;                        // threads below kGroups: a group's page,
+  bool gthere = false;                   // whether it exists,
+  uint32_t gsk = 0, gsv = 0;             // and its scales
 
-  auto k_key = [&](int u) { return (tid + u * kThreads) / (DP / 16); };
-  auto k_d = [&](int u) { return (tid + u * kThreads) % (DP / 16) * 16; };
-  auto v_kg = [&](int u) { return (tid + u * kThreads) / (DP / 4); };
-  auto v_d = [&](int u) { return (tid + u * kThreads) % (DP / 4) * 4; };
-  auto page_of = [&](int key) {
-    return key < all_hi ? max(kv::page_at(kv, b, key >> kv.page_shift), 0) : 0;
+  // Page numbers are loaded one tile before they are used and looked at only
+  // then: a look at once would wait for that load, and with it for all the
+  // loads before it.
+  const int32_t* const table = kv.table + long(b) * kv.table_ld;
+  auto unit_key = [&](int tl, int u) { return tl * kKeys + wave * kWaveKeys + u * kUnitKeys; };
+  auto entry_of = [&](int key) {
+    return min(max(min(key, all_hi - 1), 0) >> kv.page_shift, kv.max_pages - 1);
   };
-  auto load_pages = [&](int tl) {
+  auto exists = [&](int page) { return page >= 0 && page < kv.num_pages; };
+  // one page's keys or values of the head, as a buffer
+  const int block_bytes = int(head_bytes);
+  auto load_k = [&](int tl) {
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
-      kpage[u] = page_of(tl * kKeys + k_key(u));
-      vpage[u] = page_of(tl * kKeys + v_kg(u) * 4);
-    }
-    if (tid < kGroups) {
-      const int key = tl * kKeys + tid * 16;
-      gpage = key < all_hi ? kv::page_at(kv, b, key >> kv.page_shift) : -1;
+      const auto rsrc = tile::make_rsrc(k_base + long(exists(kpage[u]) ? kpage[u] : 0) * kv.page_stride, block_bytes);
+      const int at = (unit_key(tl, u) & slot_mask) * kv.dim;
+      kreg[u] = u32x4{0, 0, 0, 0};
+      if (k_there) kreg[u] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, k_off, at, 0);
     }
   };
-  auto load_tile = [&](int tl) {
+  auto load_v = [&](int tl) {
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
-      const int key = tl * kKeys + k_key(u), d = k_d(u);
-      const int8_t* src = kv.data + long(kpage[u]) * kv.page_stride + head * head_bytes +
-                          long(key & slot_mask) * kv.dim + d;
-      kreg[u] = uint4{0, 0, 0, 0};
-      if (!PAD || d < kv.dim) kreg[u] = *reinterpret_cast<const uint4*>(src);
-      const int vkey = tl * kKeys + v_kg(u) * 4, vd = v_d(u);
-      const int8_t* vs = kv.data + long(vpage[u]) * kv.page_stride +
-                         (kv.kv_heads + head) * head_bytes + long(vkey & slot_mask) * kv.dim + vd;
-      vreg[u] = uint4{0, 0, 0, 0};
-      if (!PAD || vd < kv.dim) {
-        vreg[u].x = *reinterpret_cast<const uint32_t*>(vs);
-        vreg[u].y = *reinterpret_cast<const uint32_t*>(vs + kv.dim);
-        vreg[u].z = *reinterpret_cast<const uint32_t*>(vs + 2 * kv.dim);
-        vreg[u].w = *reinterpret_cast<const uint32_t*>(vs + 3 * kv.dim);
+      const auto rsrc = tile::make_rsrc(v_base + long(exists(vpage[u]) ? vpage[u] : 0) * kv.page_stride, block_bytes);
+      const int at = (unit_key(tl, u) & slot_mask) * kv.dim;
+      vreg[u] = u32x4{0, 0, 0, 0};
+      if (v_there) {
+        vreg[u].x = __builtin_amdgcn_raw_buffer_load_b32(rsrc, v_off, at, 0);
+        vreg[u].y = __builtin_amdgcn_raw_buffer_load_b32(rsrc, v_off, at + kv.dim, 0);
+        vreg[u].z = __builtin_amdgcn_raw_buffer_load_b32(rsrc, v_off, at + 2 * kv.dim, 0);
+        vreg[u].w = __builtin_amdgcn_raw_buffer_load_b32(rsrc, v_off, at + 3 * kv.dim, 0);
       }
     }
+  };
+  auto load_scales = [&](int tl) {
     if (tid < kGroups) {
-      gthere = gpage;
-      const uint16_t* sc = kv.scale + long(max(gpage, 0)) * kv.scale_stride + head;
+      gthere = tl * kKeys + tid * 16 < all_hi && exists(gpage);
+      const uint16_t* sc = kv.scale + long(gthere ? gpage : 0) * kv.scale_stride + head;
       gsk = sc[0];
       gsv = sc[kv.kv_heads];
     }
   };
-  auto stage_tile = [&](int buf) {
+  auto load_k_pages = [&](int tl) {
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int key = k_key(u), c = k_d(u) / 8;
-      sh_k[buf][k_chunk<DP>(key, c)] = codes8(biased(kreg[u].x), biased(kreg[u].y));
-      sh_k[buf][k_chunk<DP>(key, c + 1)] = codes8(biased(kreg[u].z), biased(kreg[u].w));
-      const int kg = v_kg(u), d = v_d(u), g = kg & 3;
-      const int c2 = (kg >> 2) * 2 + (g & 1);
-      const uint32_t w0 = biased(vreg[u].x), w1 = biased(vreg[u].y), w2 = biased(vreg[u].z),
-                     w3 = biased(vreg[u].w);
-#define W4A8_COLUMN(B)                                                                   \
-  {                                                                                      \
-    typedef _Float16 half4_t __attribute__((ext_vector_type(4)));                        \
-    const half2_t lo = codes2(pair_bytes<B>(w0, w1)), hi = codes2(pair_bytes<B>(w2, w3)); \
-    half4_t four = {lo[0], lo[1], hi[0], hi[1]};                                         \
-    reinterpret_cast<half4_t*>(&sh_v[buf][v_chunk(d + B, c2)])[g >> 1] = four;           \
-  }
-      W4A8_COLUMN(0)
-      W4A8_COLUMN(1)
-      W4A8_COLUMN(2)
-      W4A8_COLUMN(3)
-#undef W4A8_COLUMN
-    }
+    for (int u = 0; u < kUnits; ++u) kpage[u] = scalar_load(table + entry_of(unit_key(tl, u)));
+  };
+  // tl's value pages are its key pages, if kpage is still tl's
+  auto load_v_pages = [&](int tl) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) vpage[u] = kpage[u];
+    if (tid < kGroups) gpage = table[entry_of(tl * kKeys + tid * 16)];
+  };
+  const int k_to0 = k_place<DP>(wave * kWaveKeys + k_lane_key, k_lane_d / 8);
+  const int k_to1 = k_place<DP>(wave * kWaveKeys + k_lane_key, k_lane_d / 8 + 1);
+  // Staging, in parts that fit between matrix instructions: half of a unit's
+  // keys, one column of a unit's values.
+  auto stage_k_part = [&](int buf, int u, int half) {
+    uint8_t* dst = sh_k + buf * kTileBytes + u * kUnitKeys * DP * 2;
+    if (half == 0)
+      *reinterpret_cast<half8_t*>(dst + k_to0) = codes8(biased(kreg[u].x), biased(kreg[u].y));
+    else
+      *reinterpret_cast<half8_t*>(dst + k_to1) = codes8(biased(kreg[u].z), biased(kreg[u].w));
+  };
+  auto stage_v_part = [&](int buf, int u, int col) {
+    typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+    const int kg = (wave * kWaveKeys + v_lane_key + u * kUnitKeys) >> 2, g = kg & 3;
+    const int c = (kg >> 2) * 2 + (g & 1);
+    const uint32_t sel = 0x0c040c00u + 0x00010001u * col;     // byte `col` of two words
+    const half2_t lo = codes2(__builtin_amdgcn_perm(biased(vreg[u].y), biased(vreg[u].x), sel));
+    const half2_t hi = codes2(__builtin_amdgcn_perm(biased(vreg[u].w), biased(vreg[u].z), sel));
+    const half4_t four = {lo[0], lo[1], hi[0], hi[1]};
+    *reinterpret_cast<half4_t*>(sh_v + buf * kTileBytes + v_place<kKeys>(v_lane_d + col, c) +
+                                8 * (g >> 1)) = four;
+  };
+  auto stage_k = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < 2 * kUnits; ++i) stage_k_part(buf, i >> 1, i & 1);
+  };
+  auto stage_v = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < 4 * kUnits; ++i) stage_v_part(buf, i >> 2, i & 3);
+  };
+  auto stage_scales = [&](int buf) {
     if (tid < kGroups) {
       // a group that is not there has weights exp2(-inf) = 0
       GroupScale g = {0.0f, -__builtin_inff(), 0.0f, 0.0f};
-      if (gthere >= 0) {
-        const float sv = h2f(gsv);
+      if (gthere) {
+        const float sv = h2f(uint16_t(gsv));
         const float sv1 = sv == 0.0f ? 0x1p-24f : sv;   // as in paged_attn.hip
-        g.sk = h2f(gsk) * factor;
+        g.sk = h2f(uint16_t(gsk)) * factor;
         g.lv = __builtin_amdgcn_logf(sv1);
         g.rv = __builtin_amdgcn_rcpf(sv1);
       }
@@ -247,92 +303,192 @@ __global__ __launch_bounds__(64 * NW, DP == 128 ? 2 : 1) void attn_tile_kernel(A
     for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
   float m = kNone, l = 0.0f;
 
-  if (first < last) {
-    load_pages(first);
-    load_tile(first);
-    load_pages(first + 1);
-    stage_tile(0);
-    load_tile(first + 1);
-    load_pages(first + 2);
-  }
-  __syncthreads();
-  for (int tl = first; tl < last; ++tl) {
-    const int buf = (tl - first) & 1;
-    if (tl + 1 < last) {
-      stage_tile(buf ^ 1);
-      load_tile(tl + 2);
-      load_pages(tl + 3);
+  // Both products read one LDS operand per matrix instruction, kAhead
+  // instructions in front; `between(i)` follows instruction i.  The order is
+  // fixed here, by barriers to the compiler's scheduler.  The chunk's part
+  // of an address is an exclusive or that can follow the buffer's addition
+  // (buffers are multiples of 1024 bytes).
+  constexpr int kAhead = 6;
+  f32x16 acc[SUB];
+  half8_t pt[kGroups];
+  constexpr int kScores = kSteps * SUB, kWeighs = kGroups * kDTiles;
+  const int k_from = k_place<DP>(r32, h), v_from = v_place<kKeys>(r32, h);
+  // S^T = K Q^T for the keys in `buf`
+  auto score = [&](int buf, auto between) {
+    const int from = k_from + buf * kTileBytes;
+    auto read = [&](int n) {       // product n: step n / SUB of subtile n % SUB
+      return *reinterpret_cast<const half8_t*>(sh_k + (from ^ (n / SUB << 5)) + n % SUB * 64 * DP);
+    };
+    half8_t a[kAhead];
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) a[n] = read(n);
+    f32x16 zero;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < kScores; ++n) {
+      acc[n % SUB] = mfma32(a[n % kAhead], q[n / SUB], n < SUB ? zero : acc[n % SUB]);
+      if (n + kAhead < kScores) a[n % kAhead] = read(n + kAhead);
+      between(n);
+      __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  // O^T += V^T P^T for the values in `buf`
+  auto weigh = [&](int buf, auto between) {
+    const int from = v_from + buf * kTileBytes;
+    auto read = [&](int n) {       // product n: 16 keys n / kDTiles, columns n % kDTiles
+      const int i = n % kDTiles;
+      // 32 columns on, the row's bit 5 turns chunk bit 2 (64-key rows)
+      const int turn = (2 * (n / kDTiles) ^ (kKeys == 64 ? 4 * (i & 1) : 0)) << 4;
+      return *reinterpret_cast<const half8_t*>(sh_v + (from ^ turn) + i * 64 * kKeys);
+    };
+    half8_t a[kAhead];
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) a[n] = read(n);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < kWeighs; ++n) {
+      o[n % kDTiles] = mfma32(a[n % kAhead], pt[n / kDTiles], o[n % kDTiles]);
+      if (n + kAhead < kWeighs) a[n % kAhead] = read(n + kAhead);
+      between(n);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto nothing = [](int) {};
+  // acc -> pt, with the row's maximum and sum brought up to date
+  auto soften = [&](int tl, int buf) {
     const int key0 = tl * kKeys;
-    if (key0 < w_hi && key0 + kKeys > w_lo) {           // some row of the wave sees some key
-      f32x16 acc[2];
+    GroupScale g[kGroups];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+    for (int n = 0; n < kGroups; ++n) g[n] = sh_s[buf][n];
+    if (key0 + kKeys > w_all_hi || key0 < w_all_lo) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[u][i] = 0.0f;
+      for (int u = 0; u < SUB; ++u)
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          acc[u] = mfma32(sh_k[buf][k_chunk<DP>(32 * u + r32, 2 * i + h)], q[i], acc[u]);
-
-      GroupScale g[kGroups];
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) g[i] = sh_s[buf][i];
-      if (key0 + kKeys > w_all_hi || key0 < w_all_lo) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int key = key0 + 32 * u + 8 * (i >> 2) + 4 * h + (i & 3);
-            const GroupScale& gs = g[2 * u + (i >> 3)];
-            // a key that is not seen is gone here, whatever its page's scale
-            acc[u][i] = key >= see_lo && key < see_hi ? __builtin_fmaf(acc[u][i], gs.sk, gs.lv)
-                                                      : -__builtin_inff();
-          }
-#pragma unroll
-        for (int n = 0; n < kGroups; ++n) g[n].sk = 1.0f, g[n].lv = 0.0f;
-      }
-      // the row's largest score: within 16 keys the largest product's, as
-      // the factor is >= 0
-      float mx = -__builtin_inff();
-#pragma unroll
-      for (int n = 0; n < kGroups; ++n) {
-        float top = acc[n >> 1][8 * (n & 1)];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, acc[n >> 1][8 * (n & 1) + i]);
-        mx = fmaxf(mx, __builtin_fmaf(top, g[n].sk, g[n].lv));
-      }
-      mx = pair_max(mx);
-      if (__ballot(mx > m + kRoom)) {
-        const float m_new = fmaxf(m, mx - kLift);
-        const float alpha = __builtin_amdgcn_exp2f(m - m_new);
-        m = m_new;
-        l *= alpha;
-#pragma unroll
-        for (int j = 0; j < kDTiles; ++j) o[j] *= alpha;
-      }
-      half8_t pt[kGroups];
-#pragma unroll
-      for (int n = 0; n < kGroups; ++n) {
-        const float c = g[n].lv - m;
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[n >> 1][8 * (n & 1) + i], g[n].sk, c));
-          sum += e;
-          pt[n][i] = static_cast<_Float16>(e);
+        for (int i = 0; i < 16; ++i) {
+          const int key = key0 + 32 * u + 8 * (i >> 2) + 4 * h + (i & 3);
+          const GroupScale& gs = g[2 * u + (i >> 3)];
+          // a key that is not seen is gone here, whatever its page's scale
+          acc[u][i] = key >= see_lo && key < see_hi ? __builtin_fmaf(acc[u][i], gs.sk, gs.lv)
+                                                    : -__builtin_inff();
         }
-        l += sum == 0.0f ? 0.0f : sum * g[n].rv;
-      }
 #pragma unroll
-      for (int n = 0; n < kGroups; ++n)
-#pragma unroll
-        for (int j = 0; j < kDTiles; ++j)
-          o[j] = mfma32(sh_v[buf][v_chunk(32 * j + r32, 2 * n + h)], pt[n], o[j]);
+      for (int n = 0; n < kGroups; ++n) g[n].sk = 1.0f, g[n].lv = 0.0f;
     }
-    __syncthreads();
+    // the row's largest score: within 16 keys the largest product's, as the
+    // factor is >= 0
+    float mx = -__builtin_inff();
+#pragma unroll
+    for (int n = 0; n < kGroups; ++n) {
+      float top = acc[n >> 1][8 * (n & 1)];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, acc[n >> 1][8 * (n & 1) + i]);
+      mx = fmaxf(mx, __builtin_fmaf(top, g[n].sk, g[n].lv));
+    }
+    mx = pair_max(mx);
+    // a row moves its maximum only when a weight would leave fp16's range
+    if (__ballot(mx > m + kRoom)) {
+      const float m_new = fmaxf(m, mx - kLift);
+      const float alpha = __builtin_amdgcn_exp2f(m - m_new);
+      m = m_new;
+      l *= alpha;
+#pragma unroll
+      for (int i = 0; i < kDTiles; ++i) o[i] *= alpha;
+    }
+#pragma unroll
+    for (int n = 0; n < kGroups; ++n) {
+      const float c = g[n].lv - m;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[n >> 1][8 * (n & 1) + i], g[n].sk, c));
+        sum += e;
+        pt[n][i] = static_cast<_Float16>(e);
+      }
+      l += sum == 0.0f ? 0.0f : sum * g[n].rv;
+    }
+  };
+
+  // Each tile is a stretch of vector work (softmax of its scores) and one of
+  // matrix work (its values, the next tile's scores), with the staging of
+  // later tiles between the matrix instructions.  With 8 waves the second
+  // four run one stretch behind the first, so that on every SIMD one wave's
+  // products run beside the other's softmax; a barrier after every stretch
+  // keeps them in step.
+  // At tile t's matrix stretch keys of t + 2 and values of t + 1 are staged,
+  // into the buffers of t's keys and t - 1's values: both halves have then
+  // read those for the last time, and the barrier after the second half's
+  // stretch comes before anyone reads the new ones.
+  constexpr bool kTwoHalves = NW == 8;
+  const bool behind = kTwoHalves && wave >= NW / 2;
+  if (first < last) {
+    load_k_pages(first);
+    load_k(first);
+    load_v_pages(first);
+    load_v(first);
+    load_k_pages(first + 1);
+    load_scales(first);
+    stage_k(0);
+    stage_v(0);
+    stage_scales(0);
+    load_k(first + 1);
+    load_v_pages(first + 1);
+    load_v(first + 1);
+    load_scales(first + 1);
+    load_k_pages(first + 2);
+    stage_k(1);
+    load_k(first + 2);
+    load_v_pages(first + 2);
+    load_k_pages(first + 3);
   }
+  lds_barrier();
+  if (w_first == first && w_first < w_last) {
+    score(0, nothing);
+  }
+  if (behind) lds_barrier();
+  int buf = 0;
+  for (int tl = first; tl < last; ++tl) {
+    // asked for first: the barriers wait for scalar loads as well
+    int later[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) later[u] = scalar_load(table + entry_of(unit_key(tl + 4, u)));
+    const bool mine = tl >= w_first && tl < w_last;
+    const bool mine_next = tl + 1 >= w_first && tl + 1 < w_last;
+    if (mine) soften(tl, buf);
+    if (kTwoHalves) {
+      lds_barrier();
+      __builtin_amdgcn_s_setprio(1);
+    }
+    // one part of the staging to every kApart products
+    if (mine) {
+      constexpr int kApart = kWeighs / (4 * kUnits) < 1 ? 1 : kWeighs / (4 * kUnits);
+      weigh(buf, [&](int n) {
+        if (n % kApart == 0 && n / kApart < 4 * kUnits) stage_v_part(buf ^ 1, n / kApart / 4, n / kApart % 4);
+      });
+    } else {
+      stage_v(buf ^ 1);
+    }
+    load_v(tl + 2);
+    if (mine_next) {
+      constexpr int kApart = kScores / (2 * kUnits) < 1 ? 1 : kScores / (2 * kUnits);
+      score(buf ^ 1, [&](int n) {
+        if (n % kApart == 0 && n / kApart < 2 * kUnits) stage_k_part(buf, n / kApart / 2, n / kApart % 2);
+      });
+    } else {
+      stage_k(buf);
+    }
+    load_k(tl + 3);
+    stage_scales(buf ^ 1);
+    load_scales(tl + 2);
+    load_v_pages(tl + 3);
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) kpage[u] = later[u];
+    if (kTwoHalves) __builtin_amdgcn_s_setprio(0);
+    lds_barrier();
+    buf ^= 1;
+  }
+  if (kTwoHalves && !behind) lds_barrier();
   l = pair_sum(l);
   if (!row_ok) return;
 
@@ -378,17 +534,17 @@ hipError_t launch_paged_attn_tile(const AttnParams& p, int waves, hipStream_t st
   if (wgs > 2147483647l) return hipErrorInvalidValue;
   const void* fn;
   if (dim <= 64)
-    fn = dim == 64 ? reinterpret_cast<const void*>(&attn_tile_kernel<64, false, 4>)
-                   : reinterpret_cast<const void*>(&attn_tile_kernel<64, true, 4>);
+    fn = dim == 64 ? reinterpret_cast<const void*>(&attn_tile_kernel<64, false, 4, 2>)
+                   : reinterpret_cast<const void*>(&attn_tile_kernel<64, true, 4, 2>);
   else if (dim > 128)
-    fn = dim == 256 ? reinterpret_cast<const void*>(&attn_tile_kernel<256, false, 4>)
-                    : reinterpret_cast<const void*>(&attn_tile_kernel<256, true, 4>);
+    fn = dim == 256 ? reinterpret_cast<const void*>(&attn_tile_kernel<256, false, 4, 1>)
+                    : reinterpret_cast<const void*>(&attn_tile_kernel<256, true, 4, 1>);
   else if (waves == 8)
-    fn = dim == 128 ? reinterpret_cast<const void*>(&attn_tile_kernel<128, false, 8>)
-                    : reinterpret_cast<const void*>(&attn_tile_kernel<128, true, 8>);
+    fn = dim == 128 ? reinterpret_cast<const void*>(&attn_tile_kernel<128, false, 8, 2>)
+                    : reinterpret_cast<const void*>(&attn_tile_kernel<128, true, 8, 2>);
   else
-    fn = dim == 128 ? reinterpret_cast<const void*>(&attn_tile_kernel<128, false, 4>)
-                    : reinterpret_cast<const void*>(&attn_tile_kernel<128, true, 4>);
+    fn = dim == 128 ? reinterpret_cast<const void*>(&attn_tile_kernel<128, false, 4, 1>)
+                    : reinterpret_cast<const void*>(&attn_tile_kernel<128, true, 4, 1>);
   return hipLaunchKernel(fn, dim3(unsigned(wgs)), dim3(64 * waves), args, 0, stream);
 }
 
