@@ -36,8 +36,9 @@ using namespace dev;
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// Weights above 2^kRoom make a row move its maximum (fp16 ends at 2^16).
-constexpr float kRoom = 15.0f;
+// A lane's weights of a tile may add up to this (fp16 ends at 65504; a weight
+// beyond it is infinite, and so is the sum).
+constexpr float kMost = 65000.0f;
 
 __device__ __forceinline__ f32x16 mfma32(half8_t a, half8_t b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
@@ -303,111 +304,127 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
     for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
   float m = kNone, l = 0.0f;
 
-  // Both products read one LDS operand per matrix instruction, kAhead
-  // instructions in front; `between(i)` follows instruction i.  The order is
-  // fixed here, by barriers to the compiler's scheduler.  The chunk's part
-  // of an address is an exclusive or that can follow the buffer's addition
-  // (buffers are multiples of 1024 bytes).
+  // The matrix instructions of a tile: numbers 0 .. kWeighs - 1 add its
+  // values, O^T += V^T P^T, and the kScores after them make the next tile's
+  // scores, S^T = K Q^T.  Each reads one LDS operand, kAhead instructions in
+  // front; `between(n)` follows instruction n.  The order is fixed here, by
+  // barriers to the compiler's scheduler.  The chunk's part of an address is
+  // an exclusive or that can follow the buffer's addition (buffers are
+  // multiples of 1024 bytes).
   constexpr int kAhead = 6;
+  constexpr int kWeighs = kGroups * kDTiles, kScores = kSteps * SUB;
   f32x16 acc[SUB];
   half8_t pt[kGroups];
-  constexpr int kScores = kSteps * SUB, kWeighs = kGroups * kDTiles;
+#pragma unroll
+  for (int n = 0; n < kGroups; ++n)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pt[n][i] = (_Float16)0.0f;
   const int k_from = k_place<DP>(r32, h), v_from = v_place<kKeys>(r32, h);
-  // S^T = K Q^T for the keys in `buf`
-  auto score = [&](int buf, auto between) {
-    const int from = k_from + buf * kTileBytes;
-    auto read = [&](int n) {       // product n: step n / SUB of subtile n % SUB
-      return *reinterpret_cast<const half8_t*>(sh_k + (from ^ (n / SUB << 5)) + n % SUB * 64 * DP);
+  auto products = [&](int v_buf, int k_buf, auto begin, auto end, auto between) {
+    constexpr int n0 = decltype(begin)::value, n1 = decltype(end)::value;
+    const int vf = v_from + v_buf * kTileBytes, kf = k_from + k_buf * kTileBytes;
+    auto read = [&](int n) {
+      if (n < kWeighs) {             // 16 keys n / kDTiles, 32 columns n % kDTiles
+        const int i = n % kDTiles;
+        // 32 columns on, the row's bit 5 turns chunk bit 2 (64-key rows)
+        const int turn = (2 * (n / kDTiles) ^ (kKeys == 64 ? 4 * (i & 1) : 0)) << 4;
+        return *reinterpret_cast<const half8_t*>(sh_v + (vf ^ turn) + i * 64 * kKeys);
+      }
+      const int j = n - kWeighs;     // step j / SUB of subtile j % SUB
+      return *reinterpret_cast<const half8_t*>(sh_k + (kf ^ (j / SUB << 5)) + j % SUB * 64 * DP);
     };
     half8_t a[kAhead];
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) a[n] = read(n);
+    for (int n = n0; n < n0 + kAhead; ++n) a[n % kAhead] = read(n);
     f32x16 zero;
 #pragma unroll
     for (int e = 0; e < 16; ++e) zero[e] = 0.0f;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int n = 0; n < kScores; ++n) {
-      acc[n % SUB] = mfma32(a[n % kAhead], q[n / SUB], n < SUB ? zero : acc[n % SUB]);
-      if (n + kAhead < kScores) a[n % kAhead] = read(n + kAhead);
-      between(n);
+    for (int n = n0; n < n1; ++n) {
+      if (n < kWeighs) {
+        o[n % kDTiles] = mfma32(a[n % kAhead], pt[n / kDTiles], o[n % kDTiles]);
+      } else {
+        const int j = n - kWeighs;
+        acc[j % SUB] = mfma32(a[n % kAhead], q[j / SUB], j < SUB ? zero : acc[j % SUB]);
+      }
+      if (n + kAhead < n1) a[n % kAhead] = read(n + kAhead);
+      between(n - n0);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  // O^T += V^T P^T for the values in `buf`
-  auto weigh = [&](int buf, auto between) {
-    const int from = v_from + buf * kTileBytes;
-    auto read = [&](int n) {       // product n: 16 keys n / kDTiles, columns n % kDTiles
-      const int i = n % kDTiles;
-      // 32 columns on, the row's bit 5 turns chunk bit 2 (64-key rows)
-      const int turn = (2 * (n / kDTiles) ^ (kKeys == 64 ? 4 * (i & 1) : 0)) << 4;
-      return *reinterpret_cast<const half8_t*>(sh_v + (from ^ turn) + i * 64 * kKeys);
-    };
-    half8_t a[kAhead];
-#pragma unroll
-    for (int n = 0; n < kAhead; ++n) a[n] = read(n);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int n = 0; n < kWeighs; ++n) {
-      o[n % kDTiles] = mfma32(a[n % kAhead], pt[n / kDTiles], o[n % kDTiles]);
-      if (n + kAhead < kWeighs) a[n % kAhead] = read(n + kAhead);
-      between(n);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  auto nothing = [](int) {};
-  // acc -> pt, with the row's maximum and sum brought up to date
+  using std::integral_constant;
+  const integral_constant<int, 0> values_begin;
+  const integral_constant<int, kWeighs> scores_begin;
+  const integral_constant<int, kWeighs + kScores> scores_end;
+  // acc -> pt, and the row's sum.  Weights are taken relative to the maximum
+  // the row has (m is it, less kLift); only when a sum shows that one of
+  // them may leave fp16's range, the row's maximum is looked for and moved, and
+  // the weights are taken again.
+  // That happens in the first tile and rarely after, so the usual tile
+  // needs no maximum and no exchange between lanes.
   auto soften = [&](int tl, int buf) {
     const int key0 = tl * kKeys;
     GroupScale g[kGroups];
 #pragma unroll
     for (int n = 0; n < kGroups; ++n) g[n] = sh_s[buf][n];
     if (key0 + kKeys > w_all_hi || key0 < w_all_lo) {
+      // a key that is not seen is gone here, whatever its page's scale
 #pragma unroll
       for (int u = 0; u < SUB; ++u)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int key = key0 + 32 * u + 8 * (i >> 2) + 4 * h + (i & 3);
           const GroupScale& gs = g[2 * u + (i >> 3)];
-          // a key that is not seen is gone here, whatever its page's scale
           acc[u][i] = key >= see_lo && key < see_hi ? __builtin_fmaf(acc[u][i], gs.sk, gs.lv)
                                                     : -__builtin_inff();
         }
 #pragma unroll
-      for (int n = 0; n < kGroups; ++n) g[n].sk = 1.0f, g[n].lv = 0.0f;
+      for (int n = 0; n < kGroups; ++n) {
+        const int key = key0 + 16 * n;
+        g[n].sk = 1.0f;
+        g[n].lv = 0.0f;
+        g[n].rv = key < see_hi && key + 16 > see_lo ? g[n].rv : 0.0f;
+      }
     }
-    // the row's largest score: within 16 keys the largest product's, as the
-    // factor is >= 0
-    float mx = -__builtin_inff();
+    float sum[kGroups];
+    auto weights = [&]() {
 #pragma unroll
-    for (int n = 0; n < kGroups; ++n) {
-      float top = acc[n >> 1][8 * (n & 1)];
+      for (int n = 0; n < kGroups; ++n) {
+        const float c = g[n].lv - m;
+        sum[n] = 0.0f;
 #pragma unroll
-      for (int i = 1; i < 8; ++i) top = fmaxf(top, acc[n >> 1][8 * (n & 1) + i]);
-      mx = fmaxf(mx, __builtin_fmaf(top, g[n].sk, g[n].lv));
-    }
-    mx = pair_max(mx);
-    // a row moves its maximum only when a weight would leave fp16's range
-    if (__ballot(mx > m + kRoom)) {
-      const float m_new = fmaxf(m, mx - kLift);
+        for (int i = 0; i < 8; ++i) {
+          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[n >> 1][8 * (n & 1) + i], g[n].sk, c));
+          pt[n][i] = static_cast<_Float16>(e);
+        }
+        // the sum of the rounded weights, as the values get them
+#pragma unroll
+        for (int i = 0; i < 8; i += 2)
+          sum[n] = __builtin_amdgcn_fdot2(half2_t{pt[n][i], pt[n][i + 1]}, half2_t{(_Float16)1.0f, (_Float16)1.0f}, sum[n], false);
+      }
+    };
+    weights();
+    float most = sum[0];
+#pragma unroll
+    for (int n = 1; n < kGroups; ++n) most += sum[n];
+    if (__ballot(!(most <= kMost))) {
+      float mx = -__builtin_inff();
+#pragma unroll
+      for (int n = 0; n < kGroups; ++n)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          mx = fmaxf(mx, __builtin_fmaf(acc[n >> 1][8 * (n & 1) + i], g[n].sk, g[n].lv));
+      const float m_new = fmaxf(m, pair_max(mx) - kLift);
       const float alpha = __builtin_amdgcn_exp2f(m - m_new);
       m = m_new;
       l *= alpha;
 #pragma unroll
       for (int i = 0; i < kDTiles; ++i) o[i] *= alpha;
+      weights();
     }
 #pragma unroll
-    for (int n = 0; n < kGroups; ++n) {
-      const float c = g[n].lv - m;
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[n >> 1][8 * (n & 1) + i], g[n].sk, c));
-        sum += e;
-        pt[n][i] = static_cast<_Float16>(e);
-      }
-      l += sum == 0.0f ? 0.0f : sum * g[n].rv;
-    }
+    for (int n = 0; n < kGroups; ++n) l = __builtin_fmaf(sum[n], g[n].rv, l);
   };
 
   // Each tile is a stretch of vector work (softmax of its scores) and one of
@@ -443,9 +460,8 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
     load_k_pages(first + 3);
   }
   lds_barrier();
-  if (w_first == first && w_first < w_last) {
-    score(0, nothing);
-  }
+  if (w_first == first && w_first < w_last)
+    products(0, 0, scores_begin, scores_end, [](int) {});
   if (behind) lds_barrier();
   int buf = 0;
   for (int tl = first; tl < last; ++tl) {
@@ -460,25 +476,27 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
       lds_barrier();
       __builtin_amdgcn_s_setprio(1);
     }
-    // one part of the staging to every kApart products
-    if (mine) {
-      constexpr int kApart = kWeighs / (4 * kUnits) < 1 ? 1 : kWeighs / (4 * kUnits);
-      weigh(buf, [&](int n) {
-        if (n % kApart == 0 && n / kApart < 4 * kUnits) stage_v_part(buf ^ 1, n / kApart / 4, n / kApart % 4);
+    // what goes between: the staging, part by part, and the loads of later
+    // tiles, each after its registers are free
+    constexpr int kJobs = 6 * kUnits + 4;
+    auto job = [&](int i) {
+      if (i < 4 * kUnits) stage_v_part(buf ^ 1, i / 4, i % 4);
+      else if (i == 4 * kUnits) load_v(tl + 2);
+      else if (i <= 6 * kUnits) stage_k_part(buf, (i - 4 * kUnits - 1) / 2, (i - 4 * kUnits - 1) % 2);
+      else if (i == 6 * kUnits + 1) load_k(tl + 3);
+    };
+    if (mine || mine_next) {
+      // where only one of them is the wave's, the other half does no harm: the
+      // weights are still 0, or the scores are not looked at
+      products(buf, buf ^ 1, values_begin, scores_end, [&](int n) {
+#pragma unroll
+        for (int i = 0; i < kJobs; ++i)
+          if (i * (kWeighs + kScores) / kJobs == n) job(i);
       });
     } else {
-      stage_v(buf ^ 1);
+#pragma unroll
+      for (int i = 0; i < kJobs; ++i) job(i);
     }
-    load_v(tl + 2);
-    if (mine_next) {
-      constexpr int kApart = kScores / (2 * kUnits) < 1 ? 1 : kScores / (2 * kUnits);
-      score(buf ^ 1, [&](int n) {
-        if (n % kApart == 0 && n / kApart < 2 * kUnits) stage_k_part(buf, n / kApart / 2, n / kApart % 2);
-      });
-    } else {
-      stage_k(buf);
-    }
-    load_k(tl + 3);
     stage_scales(buf ^ 1);
     load_scales(tl + 2);
     load_v_pages(tl + 3);
