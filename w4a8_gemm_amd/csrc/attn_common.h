@@ -25,6 +25,8 @@ static constexpr float kNone = -1.0e30f;
 // kLift) of the largest still register in fp16; the sum carries the same
 // factor and the quotient drops it.
 static constexpr float kLift = 10.0f;
+// Scores more than 2^kRoom above a row's maximum move it (fp16 ends at 2^16).
+static constexpr float kRoom = 15.0f;
 
 // codes as unsigned bytes (code + 128), four at a time
 static __device__ __forceinline__ uint32_t biased(uint32_t w) { return w ^ 0x80808080u; }
@@ -53,10 +55,9 @@ static __device__ __forceinline__ half8_t codes8(uint32_t lo, uint32_t hi) {
   return r;
 }
 
-// byte `B` (0..3) of two dwords as two 16-bit halves: w0's first
-template <int B>
-static __device__ __forceinline__ uint32_t pair_bytes(uint32_t w0, uint32_t w1) {
-  return __builtin_amdgcn_perm(w1, w0, 0x0c000c00u | uint32_t(B) | uint32_t(4 + B) << 16);
+// byte `col` (0..3, a constant) of two dwords as two 16-bit halves: w0's first
+static __device__ __forceinline__ uint32_t pair_bytes(uint32_t w0, uint32_t w1, int col) {
+  return __builtin_amdgcn_perm(w1, w0, 0x0c040c00u + 0x00010001u * uint32_t(col));
 }
 
 static __device__ __forceinline__ f32x4 mfma16(half8_t a, half8_t b, f32x4 c) {

@@ -63,37 +63,47 @@ w4a8_status check_view(const w4a8_kv_view* v, KvArgs* a) {
 }
 
 // What the attention launches for a batch: the kernel of 16-row tiles
-// (waves == 0) or the one of 32 rows a wave, and how many workgroups split
-// the keys of a row tile.
+// (waves == 0) or the one of 32 rows a wave, and the split of the keys.
 struct AttnPlan {
   int waves;
-  int splits;
-  size_t workspace;
+  int splits, chunk;
+  size_t ml_bytes, workspace;
 };
 
-// Keys are split over workgroups until about kTargetWgs run (two per compute
-// unit), each split keeping at least kMinKeys keys of the longest sequence.
-constexpr long kTargetWgs = 512;
-constexpr int kMinKeys = 256;
-constexpr int kMaxSplits = 64;
+constexpr long kComputeUnits = 256;
+constexpr int kMaxSplits = 256;
 
 AttnPlan plan_attn(const KvArgs& kv, int q_heads, int max_q, int max_len) {
   AttnPlan pl;
   const int group = q_heads / kv.kv_heads;
   const long rows = long(kv.cu_q ? max_q : 1) * group;
   pl.waves = 0;
-  if (rows > kAttnRows) pl.waves = kv.dim > 64 && kv.dim <= 128 && rows > 128 ? 8 : 4;
-  const int tile = pl.waves ? 32 * pl.waves : kAttnRows;
-  const long wgs = attn_tiles(kv, group, tile) * kv.kv_heads;
-  long splits = (kTargetWgs + wgs - 1) / wgs;
-  const long most = max_len / kMinKeys;
-  if (splits > most) splits = most;
-  if (splits > kMaxSplits) splits = kMaxSplits;
+  if (rows > kAttnRows) {
+    // 256 rows a workgroup (8 waves) where that fills the device, else 128
+    const bool wide = kv.dim > 64 && kv.dim <= 128;
+    pl.waves = wide && attn_tiles(kv, group, 256) * kv.kv_heads >= 3 * kComputeUnits ? 8 : 4;
+  }
+  const long units = attn_tiles(kv, group, pl.waves ? 32 * pl.waves : kAttnRows) * kv.kv_heads;
+  // Keys per split: so many that about `target` workgroups of equal work run,
+  // at least `least`.
+  const long target = (pl.waves ? 2 : 24) * kComputeUnits;
+  const long least = pl.waves ? 512 : units * max_len >= 512l * 256 ? 256 : 128;
+  long chunk = (units * max_len + target - 1) / target;
+  chunk = (chunk + least - 1) / least * least;
+  if (chunk < least) chunk = least;
+  long splits = (max_len + chunk - 1) / chunk;
+  if (splits > kMaxSplits) {
+    chunk = (max_len + kMaxSplits - 1) / kMaxSplits;
+    chunk = (chunk + least - 1) / least * least;
+    splits = (max_len + chunk - 1) / chunk;
+  }
+  if (pl.waves && units >= kComputeUnits) splits = 1;
   if (splits < 1) splits = 1;
   pl.splits = int(splits);
-  pl.workspace = splits > 1 ? size_t(kv.total_q) * size_t(q_heads) * size_t(splits) *
-                                  size_t(kv.dim + 2) * 4u
-                            : 0;
+  pl.chunk = chunk < (1 << 30) ? int(chunk) : 1 << 30;
+  const size_t parts = splits > 1 ? size_t(kv.total_q) * size_t(q_heads) * size_t(splits) : 0;
+  pl.ml_bytes = (parts * 8 + 255) / 256 * 256;
+  pl.workspace = parts > 0 ? pl.ml_bytes + parts * size_t(kv.dim) * 4 : 0;
   return pl;
 }
 
@@ -177,7 +187,9 @@ extern "C" w4a8_status w4a8_paged_attention(const uint16_t* q_dev, int ldq, int 
   p.scale_log2e = scale * 1.44269504f;
   p.window = window;
   p.splits = pl.splits;
-  p.part = static_cast<float*>(workspace_dev);
+  p.chunk = pl.chunk;
+  p.part_ml = static_cast<float2*>(workspace_dev);
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace_dev) + (pl.workspace ? pl.ml_bytes : 0));
   const hipStream_t s = static_cast<hipStream_t>(stream);
   st = device_status(pl.waves ? launch_paged_attn_tile(p, pl.waves, s) : launch_paged_attn(p, s));
   if (st != W4A8_OK || pl.splits == 1) return st;

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <hip/hip_runtime_api.h>
+#include <hip/hip_vector_types.h>
 
 #include "../../include/w4a8.h"
 
@@ -84,8 +85,10 @@ struct AttnParams {
   int q_heads, group;         // group = q_heads / kv_heads
   float scale_log2e;          // score scale * log2(e)
   int window;                 // 0: none
-  int splits;                 // workgroups that split one row tile's keys
-  float* part;                // splits > 1: partial results, see paged_attn.hip
+  int splits;                 // workgroups that split one row tile's keys,
+  int chunk;                  // and the keys of each (a multiple of 64; the last takes the rest)
+  float2* part_ml;            // splits > 1: maximum and sum of [token][query head][split],
+  float* part_o;              // and its unnormalised values, [dim] each
 };
 
 // Row tiles of the attention: the rows of a sequence and kv head are its

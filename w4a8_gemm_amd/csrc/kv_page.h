@@ -57,5 +57,24 @@ static __device__ __forceinline__ int page_at(const KvArgs& a, int b, int i) {
   return p >= 0 && p < a.num_pages ? p : -1;
 }
 
+// The keys of split `split` among [lo, hi): chunk keys from split * chunk on
+// (the last split takes all that follow).
+struct Range {
+  int lo, hi;
+};
+static __device__ __forceinline__ Range split_range(int split, int splits, int chunk, int lo,
+                                                    int hi) {
+  const long from = long(split) * chunk;
+  Range r;
+  r.lo = int(max(long(lo), min(from, long(hi))));
+  r.hi = split == splits - 1 ? hi : int(min(long(hi), from + chunk));
+  return r;
+}
+
+// 4-byte load from an address all lanes share, through the scalar cache
+static __device__ __forceinline__ int scalar_load(const int32_t* p) {
+  return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t(p));
+}
+
 }  // namespace kv
 }  // namespace w4a8

@@ -4,7 +4,8 @@
 // share keys and values and are tiled 16 at a time.  Four waves share a
 // row tile, each taking every fourth step of 32 keys straight from memory
 // into registers, and join through LDS; where there are few row tiles, the
-// keys are split over workgroups as well and attn_join_kernel joins them.
+// keys are split over workgroups as well, in chunks of the same number of
+// keys for every sequence, and attn_join_kernel joins them.
 //
 // Both products run transposed on v_mfma_f32_16x16x32_f16:
 //   S^T[key, row] = K Q^T      keys are rows of A, 16 per product
@@ -25,6 +26,7 @@
 #include "decoder_kernels.h"
 #include "kv_page.h"
 #include "quant_common.h"
+#include "tile_common.h"
 
 namespace w4a8 {
 namespace {
@@ -35,6 +37,10 @@ using namespace dev;
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kStep = 32;      // keys a wave takes at once
+constexpr long kJoinFewRows = 4096;
+
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 // maximum over the four lanes of a row (lane, lane ^ 16, lane ^ 32, ...)
 __device__ __forceinline__ float row_max(float x) {
@@ -46,31 +52,34 @@ __device__ __forceinline__ float row_sum(float x) {
   return x + __shfl_xor(x, 32);
 }
 
-// The keys of one 16-key half step: where they lie and their scales.
-struct Half {
-  const int8_t* k;    // 16 keys x dim codes
-  const int8_t* v;
-  float sk;           // key scale (with the score factor)
-  float lv, rv;       // log2 and reciprocal of the value scale
-  bool ok;            // the page exists
+// The 32 keys of a step on their way to the matrix cores: codes as loaded,
+// and the scales (raw fp16) of the two 16-key halves.
+template <int DP>
+struct Step {
+  u32x4 k[2][DP / 64];
+  uint32_t v[8][DP / 64];
+  uint32_t sk[2], sv[2];
+  bool ok[2];                   // the half's page exists
 };
-
-// Partial results of a split row: l, M and the unnormalised O, as
-// part[(token * heads + head) * splits + split][dim + 2].
 
 // DP: head dim rounded up to 64, 128 or 256.  PAD: dim < DP.
 template <int DP, bool PAD>
-__global__ __launch_bounds__(kThreads) void attn_split_kernel(AttnParams p) {
+__global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void attn_split_kernel(AttnParams p) {
   constexpr int kQuarter = DP / 4;        // K bytes of a lane and key
   constexpr int kKStep = DP / 32;         // products of one 16-key score tile
   constexpr int kCols = DP / 16;          // V columns of a lane
   constexpr int kVDwords = DP / 64;       // dwords of those columns and one key
   const KvArgs& kv = p.kv;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, quarter = lane >> 4;
 
-  const int split = blockIdx.x % p.splits;
+  // Splits fastest, turned from row tile to row tile: workgroups go round the
+  // 8 dies in turn, and without the turn a power of two of splits would give
+  // some dies only the splits that lie beyond short sequences (16 x 64
+  // heads x 4000 keys in 2 splits: 167 us, turned 125).
   const int rest = blockIdx.x / p.splits;
+  const int split = (blockIdx.x % p.splits + (rest >> 2)) % p.splits;
   const int head = rest % kv.kv_heads;
   const int tile = rest / kv.kv_heads;
   int b, nth;
@@ -85,24 +94,23 @@ __global__ __launch_bounds__(kThreads) void attn_split_kernel(AttnParams p) {
   const kv::Seq s = kv::seq_of(kv, b);
   const int rows = (s.hi - s.lo) * p.group;
   if (nth < 0 || long(nth) * kAttnRows >= rows) return;   // the whole workgroup
+  const int start = s.len - (s.hi - s.lo);           // position of the first new token
   const int row = nth * kAttnRows + r16;
   const bool row_ok = row < rows;
   const int t = row / p.group;                       // new token of this lane's row
   const int q_head = head * p.group + row - t * p.group;
-  const int pos = s.len - (s.hi - s.lo) + t;
   // keys this row sees: [see_lo, see_hi)
-  const int see_hi = row_ok ? pos + 1 : 0;
-  const int see_lo = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
-  // keys the tile sees
+  const int see_hi = row_ok ? start + t + 1 : 0;
+  const int see_lo = p.window > 0 ? max(start + t - p.window + 1, 0) : 0;
+  // keys the tile sees, those of the split among them, and their steps
   const int t_first = nth * kAttnRows / p.group;
   const int t_last = (min(rows, (nth + 1) * kAttnRows) - 1) / p.group;
-  const int pos_first = s.len - (s.hi - s.lo) + t_first;
-  const int all_hi = max(s.len - (s.hi - s.lo) + t_last + 1, 0);
-  const int all_lo = p.window > 0 ? max(pos_first - p.window + 1, 0) : 0;
-  const int step0 = all_lo / kStep;
-  const int steps = max((all_hi + kStep - 1) / kStep - step0, 0);
-  const int first = step0 + int(long(steps) * split / p.splits);
-  const int last = step0 + int(long(steps) * (split + 1) / p.splits);
+  const int all_hi = max(start + t_last + 1, 0);
+  const int all_lo = p.window > 0 ? max(start + t_first - p.window + 1, 0) : 0;
+  const kv::Range range = kv::split_range(split, p.splits, p.chunk, all_lo, all_hi);
+  if (range.lo >= range.hi && p.splits > 1) return;       // not joined either
+  const int first = range.lo / kStep;
+  const int last = (range.hi + kStep - 1) / kStep;
 
   // Q^T fragments: lane's row, d = quarter * DP/4 + 8 s ..
   half8_t q[kKStep];
@@ -117,63 +125,103 @@ __global__ __launch_bounds__(kThreads) void attn_split_kernel(AttnParams p) {
     }
   }
 
+  // Loads: a half step's 16 keys lie in one page, so addresses are scalar up
+  // to the lane's fixed offset.
+  const int head_bytes = kv.dim << kv.page_shift;
+  const int8_t* const base = kv.data + long(head) * head_bytes;
+  const long v_from = long(kv.kv_heads) * head_bytes;
+  const int32_t* const table = kv.table + long(b) * kv.table_ld;
+  const int slot_mask = (1 << kv.page_shift) - 1;
+  const unsigned k_off = unsigned(r16 * kv.dim + quarter * kQuarter);
+  const unsigned v_off = unsigned(quarter * 4 * kv.dim + r16 * kCols);
+  auto fetch_pages = [&](int st, int (&page)[2]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int key = min(st * kStep + 16 * u, range.hi - 1);
+      page[u] = kv::scalar_load(table + (max(key, 0) >> kv.page_shift));
+    }
+  };
+  auto fetch = [&](int st, const int (&page)[2], Step<DP>& to) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int key = st * kStep + 16 * u;
+      to.ok[u] = key < range.hi && page[u] >= 0 && page[u] < kv.num_pages;
+      const long at = to.ok[u] ? page[u] : 0;
+      const int8_t* from = base + at * kv.page_stride;
+      const int slot = (key & slot_mask) * kv.dim;
+      const auto kr = tile::make_rsrc(from, uint32_t(head_bytes));
+      const auto vr = tile::make_rsrc(from + v_from, uint32_t(head_bytes));
+#pragma unroll
+      for (int c = 0; c < DP / 64; ++c) {
+        to.k[u][c] = u32x4{0, 0, 0, 0};
+        if (!PAD || quarter * kQuarter + 16 * c < kv.dim)
+          to.k[u][c] = __builtin_amdgcn_raw_buffer_load_b128(kr, k_off + 16 * c, slot, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t (&w)[kVDwords] = to.v[4 * u + i];
+        if (PAD) __builtin_memset(w, 0, sizeof(w));
+        if (!PAD || r16 * kCols < kv.dim) {
+          const int row_at = slot + i * kv.dim;
+          if constexpr (kVDwords == 1) {
+            w[0] = __builtin_amdgcn_raw_buffer_load_b32(vr, v_off, row_at, 0);
+          } else if constexpr (kVDwords == 2) {
+            const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(vr, v_off, row_at, 0);
+            w[0] = x[0], w[1] = x[1];
+          } else {
+            const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(vr, v_off, row_at, 0);
+            w[0] = x[0], w[1] = x[1], w[2] = x[2], w[3] = x[3];
+          }
+        }
+      }
+      const uint16_t* sc = kv.scale + at * kv.scale_stride + head;
+      to.sk[u] = sc[0];
+      to.sv[u] = sc[kv.kv_heads];
+    }
+  };
+
   f32x4 o[kCols];
 #pragma unroll
   for (int j = 0; j < kCols; ++j) o[j] = f32x4{0, 0, 0, 0};
   float m = kNone, l = 0.0f;
 
-  const long head_bytes = long(kv.dim) << kv.page_shift;
-  for (int st = first + wave; st < last; st += kWaves) {
+  auto use = [&](int st, const Step<DP>& in) {
     const int key0 = st * kStep;
-    Half hf[2];
+    // scores, with the scales of their page
+    float x[8], rv[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int key = key0 + 16 * u;
-      const int page = key < all_hi ? kv::page_at(kv, b, key >> kv.page_shift) : -1;
-      hf[u].ok = page >= 0;
-      const int at = max(page, 0);
-      const int slot = key & ((1 << kv.page_shift) - 1);
-      const int8_t* base = kv.data + long(at) * kv.page_stride + head * head_bytes + long(slot) * kv.dim;
-      hf[u].k = base;
-      hf[u].v = base + kv.kv_heads * head_bytes;
-      const uint16_t* sc = kv.scale + long(at) * kv.scale_stride + head;
-      hf[u].sk = h2f(sc[0]) * p.scale_log2e * kCodeScale;
+      const float sk = h2f(uint16_t(in.sk[u])) * p.scale_log2e * kCodeScale;
       // an all-zero page has scale 0: any positive value does, and the
       // smallest leaves the running maximum to the other pages
-      const float sv = h2f(sc[kv.kv_heads]);
+      const float sv = h2f(uint16_t(in.sv[u]));
       const float sv1 = sv == 0.0f ? 0x1p-24f : sv;
-      hf[u].lv = __builtin_amdgcn_logf(sv1);
-      hf[u].rv = __builtin_amdgcn_rcpf(sv1);
-    }
-    // scores
-    float x[8];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
+      const float lv = __builtin_amdgcn_logf(sv1);
+      rv[u] = __builtin_amdgcn_rcpf(sv1);
       f32x4 acc = {0, 0, 0, 0};
-      uint32_t w[DP / 16];
-#pragma unroll
-      for (int c = 0; c < DP / 64; ++c) {
-        const int d = quarter * kQuarter + 16 * c;
-        uint4 v = {0, 0, 0, 0};
-        if (!PAD || d < kv.dim) v = *reinterpret_cast<const uint4*>(hf[u].k + r16 * kv.dim + d);
-        w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
-      }
 #pragma unroll
       for (int i = 0; i < kKStep; ++i)
-        acc = mfma16(codes8(biased(w[2 * i]), biased(w[2 * i + 1])), q[i], acc);
+        acc = mfma16(codes8(biased(in.k[u][i / 2][2 * (i % 2)]), biased(in.k[u][i / 2][2 * (i % 2) + 1])),
+                     q[i], acc);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int key = key0 + 16 * u + quarter * 4 + i;
-        const bool seen = hf[u].ok && key >= see_lo && key < see_hi;
-        x[4 * u + i] = seen ? __builtin_fmaf(acc[i], hf[u].sk, hf[u].lv) : -__builtin_inff();
+        const bool seen = in.ok[u] && key >= see_lo && key < see_hi;
+        x[4 * u + i] = seen ? __builtin_fmaf(acc[i], sk, lv) : -__builtin_inff();
       }
     }
     float mx = x[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i]);
-    const float m_new = fmaxf(m, row_max(mx) - kLift);
-    const float alpha = __builtin_amdgcn_exp2f(m - m_new);
-    m = m_new;
+    // a row moves its maximum only when a weight would leave fp16's range
+    if (__ballot(mx > m + kRoom)) {
+      const float m_new = fmaxf(m, row_max(mx) - kLift);
+      const float alpha = __builtin_amdgcn_exp2f(m - m_new);
+      m = m_new;
+      l *= alpha;
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) o[j] *= alpha;
+    }
     half8_t pt;
     float sum[2] = {0, 0};
 #pragma unroll
@@ -182,49 +230,47 @@ __global__ __launch_bounds__(kThreads) void attn_split_kernel(AttnParams p) {
       sum[i >> 2] += e;
       pt[i] = static_cast<_Float16>(e);
     }
-    l *= alpha;
     // a sum of 0 (nothing seen) stays 0 whatever the page's scale holds
 #pragma unroll
-    for (int u = 0; u < 2; ++u) l += sum[u] == 0.0f ? 0.0f : sum[u] * hf[u].rv;
-#pragma unroll
-    for (int j = 0; j < kCols; ++j) o[j] *= alpha;
-
+    for (int u = 0; u < 2; ++u) l += sum[u] == 0.0f ? 0.0f : sum[u] * rv[u];
     // values: 8 keys x kCols columns
-    uint32_t vw[8][kVDwords];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int8_t* src = hf[i >> 2].v + (quarter * 4 + (i & 3)) * kv.dim + r16 * kCols;
-#pragma unroll
-      for (int c = 0; c < kVDwords; ++c) {
-        uint32_t v = 0;
-        if (!PAD || r16 * kCols < kv.dim) v = *reinterpret_cast<const uint32_t*>(src + 4 * c);
-        vw[i][c] = biased(v);
-      }
-    }
 #pragma unroll
     for (int c = 0; c < kVDwords; ++c) {
-#define W4A8_COLUMN(B)                                                          \
-  {                                                                             \
-    half8_t a;                                                                  \
-    _Pragma("unroll") for (int i = 0; i < 8; i += 2) {                          \
-      const half2_t two = codes2(pair_bytes<B>(vw[i][c], vw[i + 1][c]));        \
-      a[i] = two[0];                                                            \
-      a[i + 1] = two[1];                                                        \
-    }                                                                           \
-    o[4 * c + B] = mfma16(a, pt, o[4 * c + B]);                                 \
-  }
-      W4A8_COLUMN(0)
-      W4A8_COLUMN(1)
-      W4A8_COLUMN(2)
-      W4A8_COLUMN(3)
-#undef W4A8_COLUMN
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = biased(in.v[i][c]);
+#pragma unroll
+      for (int col = 0; col < 4; ++col) {
+        half8_t a;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const half2_t two = codes2(pair_bytes(w[i], w[i + 1], col));
+          a[i] = two[0];
+          a[i + 1] = two[1];
+        }
+        o[4 * c + col] = mfma16(a, pt, o[4 * c + col]);
+      }
+    }
+  };
+
+  // two steps in turn: one is used while the other's loads are under way,
+  // and the pages of the one after are asked for
+  {
+    Step<DP> even;
+    int page_e[2];
+    int st = first + wave;
+    if (st < last) fetch_pages(st, page_e);
+    while (st < last) {
+      fetch(st, page_e, even);
+      fetch_pages(st + kWaves, page_e);
+      use(st, even);
+      st += kWaves;
     }
   }
   l = row_sum(l);
 
   // O^T tile j: lane holds result rows 4 quarter + i, i.e. columns
-  // (4 quarter + i) * kCols + j of its row.  Join the four waves: two LDS
-  // arrays of statistics, then the sums themselves, 4 columns at a time.
+  // (4 quarter + i) * kCols + j of its row.  Join the four waves through LDS.
   __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
   __shared__ f32x4 sh_o[kWaves][64][kCols + 1];
   if (quarter == 0) {
@@ -244,57 +290,97 @@ __global__ __launch_bounds__(kThreads) void attn_split_kernel(AttnParams p) {
     l_all += sh_l[w][r16] * factor[w];
   }
   if (!row_ok) return;
-  const float norm = l_all > 0.0f || l_all != l_all ? kCodeScale / l_all : 0.0f;
   // wave w finishes result row i = w of each quarter: kCols columns
-  const int i = wave;
-  const int d0 = (4 * quarter + i) * kCols;
+  const int d0 = (4 * quarter + wave) * kCols;
   if (PAD && d0 >= kv.dim) return;
   float out[kCols];
 #pragma unroll
   for (int j = 0; j < kCols; ++j) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += sh_o[w][lane][j][i] * factor[w];
+    for (int w = 0; w < kWaves; ++w) v += sh_o[w][lane][j][wave] * factor[w];
     out[j] = v;
   }
   if (p.splits == 1) {
+    const float norm = l_all > 0.0f || l_all != l_all ? kCodeScale / l_all : 0.0f;
     uint16_t* dst = p.out + long(s.lo + t) * p.ldo + long(q_head) * kv.dim + d0;
 #pragma unroll
     for (int j = 0; j < kCols; ++j) dst[j] = f2h_bits(out[j] * norm);
   } else {
-    float* dst = p.part + ((long(s.lo + t) * p.q_heads + q_head) * p.splits + split) * (kv.dim + 2);
-    if (quarter == 0 && i == 0) {
-      dst[0] = l_all;
-      dst[1] = m_all;
-    }
+    const long at = (long(s.lo + t) * p.q_heads + q_head) * p.splits + split;
+    if (quarter == 0 && wave == 0) p.part_ml[at] = make_float2(m_all, l_all);
+    float4* dst = reinterpret_cast<float4*>(p.part_o + at * kv.dim + d0);
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) dst[2 + d0 + j] = out[j];
+    for (int j = 0; j < kCols; j += 4) dst[j / 4] = make_float4(out[j], out[j + 1], out[j + 2], out[j + 3]);
   }
 }
 
-// One wave per row: the row's splits, in their order.
+// The splits of a row, joined in a fixed order of sums.  WPR waves share a
+// row; each takes 64 / (dim / 4) splits at a time, dim / 4 lanes a split.
+template <int WPR>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
-  const int dim = p.kv.dim;
-  const long row = long(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (row >= long(p.kv.total_q) * p.q_heads) return;
-  const float* src = p.part + row * p.splits * (dim + 2);
+  const KvArgs& kv = p.kv;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const long row = WPR == 1 ? long(blockIdx.x) * 4 + wave : long(blockIdx.x);
+  const bool row_ok = row < long(kv.total_q) * p.q_heads;
+  const int t = row_ok ? int(row / p.q_heads) : 0;
+  const int q_head = int(row - long(t) * p.q_heads);
+  int b = t, nth = 0;
+  if (kv.cu_q) b = kv::owner(t, kv.batch, [&](int i) { return kv.cu_q[i]; }, &nth);
+  const kv::Seq s = kv::seq_of(kv, b);
+  // the splits that hold keys of this row
+  const int see_hi = max(s.len - s.hi + t + 1, 0);
+  const int see_lo = p.window > 0 ? max(see_hi - p.window, 0) : 0;
+  const int s0 = min(see_lo / p.chunk, p.splits - 1);
+  const int s1 = row_ok && see_hi > 0 ? min((see_hi - 1) / p.chunk, p.splits - 1) + 1 : s0;
+
+  const float2* ml = p.part_ml + row * p.splits;
+  const float* part = p.part_o + row * p.splits * kv.dim;
   float m = kNone;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, src[long(s) * (dim + 2) + 1]);
+  for (int i = s0 + lane; i < s1; i += 64) m = fmaxf(m, ml[i].x);
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
+  const int per = kv.dim >> 2;                  // lanes of a split
+  const int groups = 64 / per;                  // splits of a wave at once
+  const int g = lane / per, d = (lane - g * per) * 4;
+  const int team = WPR == 1 ? 0 : wave;
+  float4 sum = {0, 0, 0, 0};
   float l = 0.0f;
-  for (int s = 0; s < p.splits; ++s)
-    l += src[long(s) * (dim + 2)] * __builtin_amdgcn_exp2f(src[long(s) * (dim + 2) + 1] - m);
-  const float norm = l > 0.0f || l != l ? kCodeScale / l : 0.0f;
-  const long t = row / p.q_heads;
-  uint16_t* dst = p.out + t * p.ldo + (row - t * p.q_heads) * dim;
-  for (int d = lane; d < dim; d += 64) {
-    float v = 0.0f;
-    for (int s = 0; s < p.splits; ++s) {
-      const float* part = src + long(s) * (dim + 2);
-      v += part[2 + d] * __builtin_amdgcn_exp2f(part[1] - m);
+  if (g < groups) {
+#pragma unroll 4
+    for (int i = s0 + team * groups + g; i < s1; i += WPR * groups) {
+      const float2 a = ml[i];
+      const float4 v = *reinterpret_cast<const float4*>(part + long(i) * kv.dim + d);
+      const float f = __builtin_amdgcn_exp2f(a.x - m);
+      l += a.y * f;
+      sum.x += v.x * f;
+      sum.y += v.y * f;
+      sum.z += v.z * f;
+      sum.w += v.w * f;
     }
-    dst[d] = f2h_bits(v * norm);
   }
+  __shared__ float4 sh_sum[4][64];
+  __shared__ float sh_l[4][64];
+  sh_sum[wave][lane] = sum;
+  sh_l[wave][lane] = l;
+  __syncthreads();
+  if (!row_ok || lane >= per || (WPR > 1 && wave > 0)) return;
+  float4 all = {0, 0, 0, 0};
+  float l_all = 0.0f;
+  for (int w = 0; w < WPR; ++w)
+    for (int i = 0; i < groups; ++i) {
+      const float4 v = sh_sum[WPR == 1 ? wave : w][i * per + lane];
+      all.x += v.x;
+      all.y += v.y;
+      all.z += v.z;
+      all.w += v.w;
+      l_all += sh_l[WPR == 1 ? wave : w][i * per + lane];
+    }
+  const float norm = l_all > 0.0f || l_all != l_all ? kCodeScale / l_all : 0.0f;
+  uint2 w;
+  w.x = f2h_bits(all.x * norm) | uint32_t(f2h_bits(all.y * norm)) << 16;
+  w.y = f2h_bits(all.z * norm) | uint32_t(f2h_bits(all.w * norm)) << 16;
+  *reinterpret_cast<uint2*>(p.out + long(t) * p.ldo + long(q_head) * kv.dim + d) = w;
 }
 
 }  // namespace
@@ -318,9 +404,12 @@ hipError_t launch_paged_attn(const AttnParams& p, hipStream_t stream) {
 hipError_t launch_attn_join(const AttnParams& p, hipStream_t stream) {
   AttnParams a = p;
   void* args[] = {&a};
+  // few rows: four waves read a row's splits together
   const long rows = long(p.kv.total_q) * p.q_heads;
-  return hipLaunchKernel(reinterpret_cast<const void*>(&attn_join_kernel),
-                         dim3(unsigned((rows + 3) / 4)), dim3(256), args, 0, stream);
+  const bool few = rows <= kJoinFewRows;
+  const void* fn = few ? reinterpret_cast<const void*>(&attn_join_kernel<4>)
+                       : reinterpret_cast<const void*>(&attn_join_kernel<1>);
+  return hipLaunchKernel(fn, dim3(unsigned(few ? rows : (rows + 3) / 4)), dim3(256), args, 0, stream);
 }
 
 }  // namespace w4a8

@@ -75,11 +75,6 @@ struct GroupScale {   // of 16 keys
   float sk, lv, rv, pad;
 };
 
-// uniform 4-byte load through the scalar path
-__device__ __forceinline__ int scalar_load(const int32_t* p) {
-  return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t(p));
-}
-
 // Barrier of the workgroup that makes LDS writes visible and, unlike
 // __syncthreads, leaves loads from memory in flight.
 __device__ __forceinline__ void lds_barrier() {
@@ -155,10 +150,9 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
   const int w_all_hi = w_row1 - w_row0 == 32 ? start + w_t0 + 1 : 0;
   const int w_all_lo = p.window > 0 ? max(start + w_t1 - p.window + 1, 0) : 0;
 
-  const int tile0 = all_lo / kKeys;
-  const int n_tiles = max((all_hi + kKeys - 1) / kKeys - tile0, 0);
-  const int first = tile0 + int(long(n_tiles) * split / p.splits);
-  const int last = tile0 + int(long(n_tiles) * (split + 1) / p.splits);
+  const kv::Range range = kv::split_range(split, p.splits, p.chunk, all_lo, all_hi);
+  if (range.lo >= range.hi && p.splits > 1) return;     // not joined either
+  const int first = range.lo / kKeys, last = (range.hi + kKeys - 1) / kKeys;
   // the tiles among them that some row of the wave sees
   const int w_first = max(first, w_lo / kKeys);
   const int w_last = min(last, (w_hi + kKeys - 1) / kKeys);
@@ -244,7 +238,7 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
   };
   auto load_k_pages = [&](int tl) {
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) kpage[u] = scalar_load(table + entry_of(unit_key(tl, u)));
+    for (int u = 0; u < kUnits; ++u) kpage[u] = kv::scalar_load(table + entry_of(unit_key(tl, u)));
   };
   // tl's value pages are its key pages, if kpage is still tl's
   auto load_v_pages = [&](int tl) {
@@ -468,7 +462,7 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
     // asked for first: the barriers wait for scalar loads as well
     int later[kUnits];
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) later[u] = scalar_load(table + entry_of(unit_key(tl + 4, u)));
+    for (int u = 0; u < kUnits; ++u) later[u] = kv::scalar_load(table + entry_of(unit_key(tl + 4, u)));
     const bool mine = tl >= w_first && tl < w_last;
     const bool mine_next = tl + 1 >= w_first && tl + 1 < w_last;
     if (mine) soften(tl, buf);
@@ -526,17 +520,16 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
         *reinterpret_cast<uint2*>(dst + d) = w;
       }
   } else {
-    float* dst = p.part + ((long(s.lo + t) * p.q_heads + q_head) * p.splits + split) * (kv.dim + 2);
-    if (h == 0) {
-      dst[0] = l;
-      dst[1] = m;
-    }
+    const long at = (long(s.lo + t) * p.q_heads + q_head) * p.splits + split;
+    if (h == 0) p.part_ml[at] = make_float2(m, l);
+    float* dst = p.part_o + at * kv.dim;
 #pragma unroll
     for (int j = 0; j < kDTiles; ++j)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int d = 32 * j + 8 * (i >> 2) + 4 * h + (i & 3);
-        if (!PAD || d < kv.dim) dst[2 + d] = o[j][i];
+      for (int i = 0; i < 16; i += 4) {
+        const int d = 32 * j + 2 * i + 4 * h;
+        if (!PAD || d < kv.dim)
+          *reinterpret_cast<float4*>(dst + d) = make_float4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]);
       }
   }
 }

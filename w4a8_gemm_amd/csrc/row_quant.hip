@@ -19,8 +19,8 @@ namespace {
 
 using namespace dev;
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
+constexpr int kManyRows = 512;
+constexpr int kThreads = 256;      // of the kernels for long or unaligned rows
 
 // |v| as an unsigned integer: ordered like the magnitude, with infinity above
 // every finite value and NaN above infinity, so a maximum keeps both
@@ -87,6 +87,122 @@ __device__ __forceinline__ void store8c(int8_t* dst, int i, int k, const float (
   }
 }
 
+// Largest |y| (as abs_bits) and the sum over a workgroup of T threads, in
+// every thread; always added in the same order.
+template <int T>
+__device__ __forceinline__ void reduce(float& sum, uint32_t& mx) {
+  __shared__ float sums[T / 64];
+  __shared__ uint32_t maxs[T / 64];
+  sum = wave_sum(sum);
+  mx = wave_max_u32(mx);
+  if ((threadIdx.x & 63) == 0) {
+    sums[threadIdx.x >> 6] = sum;
+    maxs[threadIdx.x >> 6] = mx;
+  }
+  __syncthreads();
+  sum = 0.0f;
+  mx = 0;
+#pragma unroll
+  for (int i = 0; i < T / 64; ++i) {
+    sum += sums[i];
+    mx = max(mx, maxs[i]);
+  }
+}
+
+// eight codes under the multiplier r, one 8-byte store
+__device__ __forceinline__ void store_codes(int8_t* dst, const float (&y)[8], float r) {
+  uint32_t b[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) b[j] = code_byte(y[j], r);
+  uint2 o;
+  o.x = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u) | __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+  o.y = __builtin_amdgcn_perm(b[5], b[4], 0x0c0c0400u) | __builtin_amdgcn_perm(b[7], b[6], 0x04000c0cu);
+  *reinterpret_cast<uint2*>(dst) = o;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
+  uint16_t v[8];
+  __builtin_memcpy(v, &u, 16);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = h2f(v[j]);
+}
+
+// Rows that T threads hold in CH chunks of 8 values each: read once, all
+// loads in flight together.
+template <int T, int CH>
+__global__ __launch_bounds__(T) void rms_norm_quant_held_kernel(NormParams p) {
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const uint16_t* x = p.x + size_t(row) * size_t(p.ldx);
+  uint4 v[CH], w[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = (c * T + tid) * 8;
+    v[c] = i < p.k ? *reinterpret_cast<const uint4*>(x + i) : uint4{0, 0, 0, 0};
+  }
+  if (p.residual) {
+    const uint16_t* res = p.residual + size_t(row) * size_t(p.ldr);
+    uint4 u[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = (c * T + tid) * 8;
+      u[c] = i < p.k ? *reinterpret_cast<const uint4*>(res + i) : uint4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float a[8], b[8];
+      unpack8(v[c], a);
+      unpack8(u[c], b);
+      uint16_t s[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = f2h_bits(a[j] + b[j]);
+      __builtin_memcpy(&v[c], s, 16);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = (c * T + tid) * 8;
+    w[c] = i < p.k ? *reinterpret_cast<const uint4*>(p.weight + i) : uint4{0, 0, 0, 0};
+  }
+  if (p.h) {
+    uint16_t* h = p.h + size_t(row) * size_t(p.ldh);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = (c * T + tid) * 8;
+      if (i < p.k) *reinterpret_cast<uint4*>(h + i) = v[c];
+    }
+  }
+  float sum = 0.0f;
+  uint32_t mx = 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    float f[8], g[8];
+    unpack8(v[c], f);
+    unpack8(w[c], g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      sum = __builtin_fmaf(f[j], f[j], sum);
+      mx = max(mx, abs_bits(f[j] * g[j]));
+    }
+  }
+  reduce<T>(sum, mx);
+  const float rstd = 1.0f / __builtin_sqrtf(sum / float(p.k) + p.eps);
+  const uint16_t sb = scale_bits_of(rstd * __builtin_bit_cast(float, mx));
+  if (tid == 0) p.s_a[row] = sb;
+  const float r = act_recip(sb);
+  int8_t* a8 = p.a8 + size_t(row) * size_t(p.lda8);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = (c * T + tid) * 8;
+    if (i >= p.k) continue;
+    float f[8], g[8], y[8];
+    unpack8(v[c], f);
+    unpack8(w[c], g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = rstd * (f[j] * g[j]);
+    store_codes(a8 + i, y, r);
+  }
+}
+
 template <bool VEC>
 __global__ __launch_bounds__(kThreads) void rms_norm_quant_kernel(NormParams p) {
   const int row = blockIdx.x, tid = threadIdx.x;
@@ -115,22 +231,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_quant_kernel(NormParams p) 
       mx = max(mx, abs_bits(f * h2f(w[j])));
     }
   }
-  __shared__ float wave_sums[kWaves];
-  __shared__ uint32_t wave_maxs[kWaves];
-  sum = wave_sum(sum);
-  mx = wave_max_u32(mx);
-  if ((tid & 63) == 0) {
-    wave_sums[tid >> 6] = sum;
-    wave_maxs[tid >> 6] = mx;
-  }
-  __syncthreads();
-  sum = 0.0f;
-  mx = 0;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    sum += wave_sums[i];
-    mx = max(mx, wave_maxs[i]);
-  }
+  reduce<kThreads>(sum, mx);
   const float rstd = 1.0f / __builtin_sqrtf(sum / float(p.k) + p.eps);
   const uint16_t sb = scale_bits_of(rstd * __builtin_bit_cast(float, mx));
   if (tid == 0) p.s_a[row] = sb;
@@ -173,12 +274,8 @@ __global__ __launch_bounds__(kThreads) void silu_mul_quant_kernel(SwigluParams p
 #pragma unroll
     for (int j = 0; j < 8; ++j) mx = max(mx, abs_bits(swiglu(g[j], u[j])));
   }
-  __shared__ uint32_t wave_maxs[kWaves];
-  mx = wave_max_u32(mx);
-  if ((tid & 63) == 0) wave_maxs[tid >> 6] = mx;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) mx = max(mx, wave_maxs[i]);
+  float unused = 0.0f;
+  reduce<kThreads>(unused, mx);
   const uint16_t sb = scale_bits_of(__builtin_bit_cast(float, mx));
   if (tid == 0) p.s_a[row] = sb;
   const float r = act_recip(sb);
@@ -194,6 +291,70 @@ __global__ __launch_bounds__(kThreads) void silu_mul_quant_kernel(SwigluParams p
   }
 }
 
+template <int T, int CH>
+__global__ __launch_bounds__(T) void silu_mul_quant_held_kernel(SwigluParams p) {
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const uint16_t* gate = p.gate + size_t(row) * size_t(p.ldg);
+  const uint16_t* up = p.up + size_t(row) * size_t(p.ldu);
+  uint4 g[CH], u[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = (c * T + tid) * 8;
+    g[c] = i < p.k ? *reinterpret_cast<const uint4*>(gate + i) : uint4{0, 0, 0, 0};
+    u[c] = i < p.k ? *reinterpret_cast<const uint4*>(up + i) : uint4{0, 0, 0, 0};
+  }
+  float y[CH][8];
+  uint32_t mx = 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    uint16_t a[8], b[8];
+    __builtin_memcpy(a, &g[c], 16);
+    __builtin_memcpy(b, &u[c], 16);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      y[c][j] = swiglu(a[j], b[j]);
+      mx = max(mx, abs_bits(y[c][j]));
+    }
+  }
+  float unused = 0.0f;
+  reduce<T>(unused, mx);
+  const uint16_t sb = scale_bits_of(__builtin_bit_cast(float, mx));
+  if (tid == 0) p.s_a[row] = sb;
+  const float r = act_recip(sb);
+  int8_t* a8 = p.a8 + size_t(row) * size_t(p.lda8);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = (c * T + tid) * 8;
+    if (i < p.k) store_codes(a8 + i, y[c], r);
+  }
+}
+
+// Threads and chunks of a held row.  With many rows a few waves a row are
+// enough and spend less on the reduction; with few, every thread takes one
+// chunk if the row allows it, so that the loads of a row are all out at once.
+struct Held {
+  int threads, chunks;      // threads 0: the row is too long
+};
+Held held_plan(int m, int k) {
+  const int n = (k + 7) / 8;
+  const int most = m >= kManyRows ? 4 : 1;
+  for (int t = 256; t <= 1024; t *= 2)
+    if (n <= most * t) return {t, (n + t - 1) / t};
+  return {n <= 4096 ? 1024 : 0, (n + 1023) / 1024};
+}
+
+#define W4A8_HELD(kernel, h)                                                        \
+  ((h).threads == 256   ? (h).chunks == 1   ? reinterpret_cast<const void*>(&kernel<256, 1>)  \
+                          : (h).chunks == 2 ? reinterpret_cast<const void*>(&kernel<256, 2>)  \
+                                            : reinterpret_cast<const void*>(&kernel<256, 4>)  \
+   : (h).threads == 512 ? (h).chunks == 1   ? reinterpret_cast<const void*>(&kernel<512, 1>)  \
+                          : (h).chunks <= 3 ? reinterpret_cast<const void*>(&kernel<512, 3>)  \
+                                            : reinterpret_cast<const void*>(&kernel<512, 4>)  \
+                        : (h).chunks == 1   ? reinterpret_cast<const void*>(&kernel<1024, 1>) \
+                          : (h).chunks == 2 ? reinterpret_cast<const void*>(&kernel<1024, 2>) \
+                          : (h).chunks == 3 ? reinterpret_cast<const void*>(&kernel<1024, 3>) \
+                                            : reinterpret_cast<const void*>(&kernel<1024, 4>))
+
 bool rows16(const void* p, int ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
 bool rows8(const void* p, int ld) { return reinterpret_cast<uintptr_t>(p) % 8 == 0 && ld % 8 == 0; }
 
@@ -205,6 +366,10 @@ hipError_t launch_rms_norm_quant(const NormParams& p, hipStream_t stream) {
                    rows8(p.a8, p.lda8);
   NormParams q = p;
   void* args[] = {&q};
+  const Held held = held_plan(p.m, p.k);
+  if (vec && held.threads)
+    return hipLaunchKernel(W4A8_HELD(rms_norm_quant_held_kernel, held), dim3(p.m),
+                           dim3(held.threads), args, 0, stream);
   const void* fn = vec ? reinterpret_cast<const void*>(&rms_norm_quant_kernel<true>)
                        : reinterpret_cast<const void*>(&rms_norm_quant_kernel<false>);
   return hipLaunchKernel(fn, dim3(p.m), dim3(kThreads), args, 0, stream);
@@ -215,6 +380,10 @@ hipError_t launch_silu_mul_quant(const SwigluParams& p, hipStream_t stream) {
                    rows8(p.a8, p.lda8);
   SwigluParams q = p;
   void* args[] = {&q};
+  const Held held = held_plan(p.m, p.k);
+  if (vec && held.threads)
+    return hipLaunchKernel(W4A8_HELD(silu_mul_quant_held_kernel, held), dim3(p.m),
+                           dim3(held.threads), args, 0, stream);
   const void* fn = vec ? reinterpret_cast<const void*>(&silu_mul_quant_kernel<true>)
                        : reinterpret_cast<const void*>(&silu_mul_quant_kernel<false>);
   return hipLaunchKernel(fn, dim3(p.m), dim3(kThreads), args, 0, stream);
