@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import sys
 
 import numpy as np
 
@@ -170,14 +171,22 @@ def unpack(blob: np.ndarray) -> dict:
 
 # ------------------------------------------------------------------ device side
 def _torch():
-    import torch
-    return torch
+    return sys.modules["torch"]      # imported by _load()
 
 
 def _stream_ptr(stream=None) -> int:
     torch = _torch()
     s = stream if stream is not None else torch.cuda.current_stream()
     return int(s.cuda_stream)
+
+
+def _stream_of(t, stream=None) -> int:
+    """The given stream, or the current one of t's device."""
+    if stream is not None:
+        return int(stream.cuda_stream)
+    # the raw handle where torch offers it: a Stream object takes 2.6 us to make
+    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    return raw(t.device.index) if raw else _stream_ptr()
 
 
 def to_device(blob: np.ndarray, device="cuda"):
@@ -370,7 +379,7 @@ def rms_norm_quant(x, weight, eps: float = 1e-5, residual=None, h=None, a8=None,
         x.data_ptr(), _ld(x), residual.data_ptr() if residual is not None else None,
         _ld(residual) if residual is not None else 0, weight.data_ptr(), eps, m, k,
         h.data_ptr() if h is not None else None, _ld(h) if h is not None else 0,
-        a8.data_ptr(), _ld(a8), s_a.data_ptr(), _stream_ptr(stream)), "w4a8_rms_norm_quant")
+        a8.data_ptr(), _ld(a8), s_a.data_ptr(), _stream_of(x, stream)), "w4a8_rms_norm_quant")
     return (h if h is not None else x), a8, s_a
 
 
@@ -390,7 +399,7 @@ def silu_mul_quant(gate, up=None, a8=None, s_a=None, stream=None):
         up_ptr, ldu = up.data_ptr(), _ld(up)
     a8, s_a = _int8_out(m, k, a8, s_a, gate.device)
     _check(lib.w4a8_silu_mul_quant(gate.data_ptr(), _ld(gate), up_ptr, ldu, m, k, a8.data_ptr(),
-                                   _ld(a8), s_a.data_ptr(), _stream_ptr(stream)),
+                                   _ld(a8), s_a.data_ptr(), _stream_of(gate, stream)),
            "w4a8_silu_mul_quant")
     return a8, s_a
 
@@ -513,7 +522,7 @@ def rope_append(q, k, v, cos_sin, cache, scale, block_table, seq_lens, cu_q=None
         q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, heads,
         cos_sin.data_ptr() if cos_sin is not None else None, rotary, max_pos, int(interleaved),
         ctypes.byref(view), out.data_ptr(), _heads("out", out, tokens, heads, dim),
-        _stream_ptr(stream)), "w4a8_rope_append")
+        _stream_of(q, stream)), "w4a8_rope_append")
     return out
 
 
@@ -537,13 +546,15 @@ def paged_attention(q, cache, scale_kv, block_table, seq_lens, cu_q=None, max_q:
     need = lib.w4a8_paged_attention_workspace_size(ctypes.byref(view), heads, max_q, max_len)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None:
+            workspace.record_stream(stream)     # freed here, in use there
     _check(lib.w4a8_paged_attention(
         q.data_ptr(), ldq, heads, ctypes.byref(view), max_q, max_len,
         dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
         _heads("out", out, tokens, heads, dim),
         workspace.data_ptr() if workspace is not None else None,
         workspace.numel() * workspace.element_size() if workspace is not None else 0,
-        _stream_ptr(stream)), "w4a8_paged_attention")
+        _stream_of(q, stream)), "w4a8_paged_attention")
     return out
 
 

@@ -47,12 +47,19 @@ __device__ __forceinline__ Item item_of(int j, int rotary, bool interleaved) {
   return it;
 }
 
-__device__ __forceinline__ void load16(const uint16_t* src, const Item& it, float (&v)[16]) {
+// an item as loaded: 16 fp16 values
+struct Raw {
+  uint4 a, b;
+};
+
+__device__ __forceinline__ Raw load_raw(const uint16_t* src, const Item& it) {
+  return {*reinterpret_cast<const uint4*>(src + it.o1), *reinterpret_cast<const uint4*>(src + it.o2)};
+}
+
+__device__ __forceinline__ void unpack16(const Raw& r, float (&v)[16]) {
   uint16_t h[16];
-  const uint4 a = *reinterpret_cast<const uint4*>(src + it.o1);
-  const uint4 b = *reinterpret_cast<const uint4*>(src + it.o2);
-  __builtin_memcpy(h, &a, 16);
-  __builtin_memcpy(h + 8, &b, 16);
+  __builtin_memcpy(h, &r.a, 16);
+  __builtin_memcpy(h + 8, &r.b, 16);
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = h2f(h[i]);
 }
@@ -108,7 +115,11 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
 }
 
 // WPB waves own a block (1: the block belongs to one wave, 4 blocks per
-// workgroup; 4: to the workgroup).
+// workgroup; 4: to the workgroup).  Up to kHeld items a thread stay in
+// registers from the search for their largest value to their quantization;
+// larger blocks are read (and rotated) twice.
+constexpr int kHeld = 2;
+
 template <int WPB>
 __device__ __forceinline__ void append_block(const AppendParams& p, int unit) {
   const KvArgs& kv = p.kv;
@@ -134,33 +145,66 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int unit) {
   const int page_begin = page_index << kv.page_shift;
   const int begin = max(start, page_begin);            // new positions in this page
   const int end = min(s.len, page_begin + (1 << kv.page_shift));
-  const int page = nth >= 0 && begin < end ? kv::page_at(kv, b, page_index) : -1;
   // every wave of a team takes the same way here
-  if (page < 0) return;
+  if (nth < 0 || begin >= end) return;
   const int first = begin - page_begin;                // slots before it hold earlier tokens
   const int count = end - begin;
   const int token0 = s.hi - (s.len - begin);           // new token at position `begin`
 
-  int8_t* block = kv.data + long(page) * kv.page_stride +
-                  (long(which * kv.kv_heads + head) << kv.page_shift) * kv.dim;
-  uint16_t* scale = kv.scale + long(page) * kv.scale_stride + which * kv.kv_heads + head;
   const uint16_t* src = (which ? p.v : p.k) + long(head) * kv.dim;
   const long ld = which ? p.ldv : p.ldk;
   const int rotary = which ? 0 : p.rotary;
   const bool inter = p.interleaved != 0;
-
-  const uint32_t old_bits = first > 0 ? *scale & 0x7FFFu : 0u;
   const int per_token = kv.dim >> 4;
   const int items = count * per_token;
-  uint32_t mx = 0;
-  for (int i = tid; i < items; i += kTeam) {
-    const int t = i / per_token;
-    const Item it = item_of(i - t * per_token, rotary, inter);
-    float v[16];
-    load16(src + (token0 + t) * ld, it, v);
+  const bool held = items <= kHeld * kTeam;
+
+  auto item = [&](int i, int* t) {
+    *t = i / per_token;
+    return item_of(i - *t * per_token, rotary, inter);
+  };
+  auto turn = [&](float (&v)[16], const Item& it, int t) {
     if (it.pair >= 0) rotate16(v, turn_of(p, it, begin + t), inter);
+  };
+  // the items' loads go out before the page's number and old scale are there
+  Raw raw[kHeld];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) mx = max(mx, __builtin_bit_cast(uint32_t, v[e]) & 0x7FFFFFFFu);
+  for (int j = 0; j < kHeld; ++j) {
+    const int i = tid + j * kTeam;
+    int t;
+    const Item it = item(i, &t);
+    if (held && i < items) raw[j] = load_raw(src + (token0 + t) * ld, it);
+  }
+  const int page = kv::page_at(kv, b, page_index);
+  if (page < 0) return;
+  int8_t* block = kv.data + long(page) * kv.page_stride +
+                  (long(which * kv.kv_heads + head) << kv.page_shift) * kv.dim;
+  uint16_t* scale = kv.scale + long(page) * kv.scale_stride + which * kv.kv_heads + head;
+  const uint32_t old_bits = first > 0 ? *scale & 0x7FFFu : 0u;
+
+  float v[kHeld][16];
+  uint32_t mx = 0;
+  if (held) {
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const int i = tid + j * kTeam;
+      if (i >= items) continue;
+      int t;
+      const Item it = item(i, &t);
+      unpack16(raw[j], v[j]);
+      turn(v[j], it, t);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mx = max(mx, __builtin_bit_cast(uint32_t, v[j][e]) & 0x7FFFFFFFu);
+    }
+  } else {
+    for (int i = tid; i < items; i += kTeam) {
+      int t;
+      const Item it = item(i, &t);
+      unpack16(load_raw(src + (token0 + t) * ld, it), v[0]);
+      turn(v[0], it, t);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mx = max(mx, __builtin_bit_cast(uint32_t, v[0][e]) & 0x7FFFFFFFu);
+    }
   }
   mx = wave_max_u32(mx);
   if (WPB > 1) {
@@ -190,24 +234,38 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int unit) {
       *at = w;
     }
   }
-  for (int i = tid; i < items; i += kTeam) {
-    const int t = i / per_token;
-    const Item it = item_of(i - t * per_token, rotary, inter);
-    float v[16];
-    load16(src + (token0 + t) * ld, it, v);
-    if (it.pair >= 0) rotate16(v, turn_of(p, it, begin + t), inter);
+  auto store = [&](const float (&y)[16], const Item& it, int t) {
     int8_t* dst = block + (first + t) * kv.dim;
-    *reinterpret_cast<uint2*>(dst + it.o1) = uint2{codes4(v, r), codes4(v + 4, r)};
-    *reinterpret_cast<uint2*>(dst + it.o2) = uint2{codes4(v + 8, r), codes4(v + 12, r)};
+    *reinterpret_cast<uint2*>(dst + it.o1) = uint2{codes4(y, r), codes4(y + 4, r)};
+    *reinterpret_cast<uint2*>(dst + it.o2) = uint2{codes4(y + 8, r), codes4(y + 12, r)};
+  };
+  if (held) {
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const int i = tid + j * kTeam;
+      if (i >= items) continue;
+      int t;
+      const Item it = item(i, &t);
+      store(v[j], it, t);
+    }
+  } else {
+    for (int i = tid; i < items; i += kTeam) {
+      int t;
+      const Item it = item(i, &t);
+      unpack16(load_raw(src + (token0 + t) * ld, it), v[0]);
+      turn(v[0], it, t);
+      store(v[0], it, t);
+    }
   }
 }
 
-// Queries: one item of one token, `heads_each` heads of it (the cosines stay
-// in registers).
-__device__ __forceinline__ void rotate_queries(const AppendParams& p, long index, int heads_each) {
+// Queries: one item of one token, HEADS heads of it (the cosines stay in
+// registers).
+template <int HEADS>
+__device__ __forceinline__ void rotate_queries(const AppendParams& p, long index) {
   const KvArgs& kv = p.kv;
   const int per_token = kv.dim >> 4;
-  const int parts = (p.q_heads + heads_each - 1) / heads_each;
+  const int parts = (p.q_heads + HEADS - 1) / HEADS;
   const int j = int(index % per_token);
   const long rest = index / per_token;
   const int part = int(rest % parts);
@@ -215,6 +273,11 @@ __device__ __forceinline__ void rotate_queries(const AppendParams& p, long index
   if (t >= kv.total_q) return;
   const bool inter = p.interleaved != 0;
   const Item it = item_of(j, p.rotary, inter);
+  const int h0 = part * HEADS;
+  Raw raw[HEADS];
+#pragma unroll
+  for (int h = 0; h < HEADS; ++h)
+    if (h0 + h < p.q_heads) raw[h] = load_raw(p.q + t * p.ldq + long(h0 + h) * kv.dim, it);
   Turn turn;
   if (it.pair >= 0) {
     int b = int(t), nth = 0;
@@ -222,10 +285,11 @@ __device__ __forceinline__ void rotate_queries(const AppendParams& p, long index
     const kv::Seq s = kv::seq_of(kv, b);
     turn = turn_of(p, it, s.len - s.hi + int(t));
   }
-  const int h1 = min(p.q_heads, (part + 1) * heads_each);
-  for (int h = part * heads_each; h < h1; ++h) {
+#pragma unroll
+  for (int h = 0; h < HEADS; ++h) {
+    if (h0 + h >= p.q_heads) continue;
     float v[16];
-    load16(p.q + t * p.ldq + long(h) * kv.dim, it, v);
+    unpack16(raw[h], v);
     if (it.pair >= 0) rotate16(v, turn, inter);
     uint16_t o[16];
 #pragma unroll
@@ -233,21 +297,21 @@ __device__ __forceinline__ void rotate_queries(const AppendParams& p, long index
     uint4 a, b4;
     __builtin_memcpy(&a, o, 16);
     __builtin_memcpy(&b4, o + 8, 16);
-    uint16_t* dst = p.q_out + t * p.ldqo + long(h) * kv.dim;
+    uint16_t* dst = p.q_out + t * p.ldqo + long(h0 + h) * kv.dim;
     *reinterpret_cast<uint4*>(dst + it.o1) = a;
     *reinterpret_cast<uint4*>(dst + it.o2) = b4;
   }
 }
 
-template <int WPB>
+template <int WPB, int HEADS>
 __global__ __launch_bounds__(kThreads) void rope_append_kernel(AppendParams p, int block_wgs,
-                                                               int units, int heads_each) {
+                                                               int units) {
   if (int(blockIdx.x) < block_wgs) {
     const int unit = WPB == 1 ? int(blockIdx.x) * 4 + (threadIdx.x >> 6) : int(blockIdx.x);
     if (unit < units) append_block<WPB>(p, unit);
     return;
   }
-  rotate_queries(p, long(blockIdx.x - block_wgs) * kThreads + threadIdx.x, heads_each);
+  rotate_queries<HEADS>(p, long(blockIdx.x - block_wgs) * kThreads + threadIdx.x);
 }
 
 }  // namespace
@@ -255,20 +319,21 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(AppendParams p, i
 hipError_t launch_rope_append(const AppendParams& p, hipStream_t stream) {
   const long slots = append_slots(p.kv);
   const long units = slots * 2 * p.kv.kv_heads;
-  // one wave per block where sequences bring few tokens each
+  // one wave per block, and one head of a query per thread, where sequences
+  // bring few tokens each
   const bool small = long(p.kv.total_q) <= 4l * p.kv.batch;
+  const int heads = small ? 1 : 4;
   const long block_wgs = small ? (units + 3) / 4 : units;
-  int heads_each = p.q_heads < 4 ? p.q_heads : 4;
-  const long parts = (p.q_heads + heads_each - 1) / heads_each;
+  const long parts = (p.q_heads + heads - 1) / heads;
   const long items = long(p.kv.total_q) * (p.kv.dim / 16) * parts;
   const long q_wgs = (items + kThreads - 1) / kThreads;
   const long wgs = block_wgs + q_wgs;
   if (units > 2147483647l || wgs > 2147483647l) return hipErrorInvalidValue;
   AppendParams a = p;
   int bw = int(block_wgs), un = int(units);
-  void* args[] = {&a, &bw, &un, &heads_each};
-  const void* fn = small ? reinterpret_cast<const void*>(&rope_append_kernel<1>)
-                         : reinterpret_cast<const void*>(&rope_append_kernel<4>);
+  void* args[] = {&a, &bw, &un};
+  const void* fn = small ? reinterpret_cast<const void*>(&rope_append_kernel<1, 1>)
+                         : reinterpret_cast<const void*>(&rope_append_kernel<4, 4>);
   return hipLaunchKernel(fn, dim3(unsigned(wgs)), dim3(kThreads), args, 0, stream);
 }
 
