@@ -435,7 +435,7 @@ typedef struct {
  * of 0 is a no-op.
  * Errors: INVALID_ARGUMENT (null or misaligned pointer, stride too small, bad
  * size), UNSUPPORTED (head_dim, page_size, rotary_dim, more than
- * W4A8_HEADS_MAX heads), DEVICE. */
+ * W4A8_HEADS_MAX heads, more work than one launch holds), DEVICE. */
 w4a8_status w4a8_rope_append(const uint16_t* q_dev, int ldq, const uint16_t* k_dev, int ldk,
                              const uint16_t* v_dev, int ldv, int q_heads,
                              const float* cos_sin_dev, int rotary_dim, int max_pos,
@@ -463,8 +463,8 @@ w4a8_status w4a8_rope_append(const uint16_t* q_dev, int ldq, const uint16_t* k_d
  * second product as fp16.  Results do not depend on scheduling (no atomics).
  * batch or total_q of 0 is a no-op.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED (as w4a8_rope_append; q_heads not a
- * multiple of kv_heads; total_q * q_heads >= 2^31), BUFFER_TOO_SMALL,
- * DEVICE. */
+ * multiple of kv_heads; more row tiles than one launch holds),
+ * BUFFER_TOO_SMALL, DEVICE. */
 size_t w4a8_paged_attention_workspace_size(const w4a8_kv_view* view, int q_heads, int max_q,
                                            int max_len);
 w4a8_status w4a8_paged_attention(const uint16_t* q_dev, int ldq, int q_heads,

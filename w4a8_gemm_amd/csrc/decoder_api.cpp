@@ -2,6 +2,7 @@
 // (host only, before any HIP call) and launch plans.
 #include <hip/hip_runtime_api.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -67,6 +68,7 @@ w4a8_status check_view(const w4a8_kv_view* v, KvArgs* a) {
 struct AttnPlan {
   int waves;
   int splits, chunk;
+  long wgs;
   size_t ml_bytes, workspace;
 };
 
@@ -85,22 +87,19 @@ AttnPlan plan_attn(const KvArgs& kv, int q_heads, int max_q, int max_len) {
   }
   const long units = attn_tiles(kv, group, pl.waves ? 32 * pl.waves : kAttnRows) * kv.kv_heads;
   // Keys per split: so many that about `target` workgroups of equal work run,
-  // at least `least`.
+  // at least `least`; none where row tiles alone fill the device, and none for
+  // more rows than one launch joins.
   const long target = (pl.waves ? 2 : 24) * kComputeUnits;
-  const long least = pl.waves ? 512 : units * max_len >= 512l * 256 ? 256 : 128;
-  long chunk = (units * max_len + target - 1) / target;
-  chunk = (chunk + least - 1) / least * least;
-  if (chunk < least) chunk = least;
-  long splits = (max_len + chunk - 1) / chunk;
-  if (splits > kMaxSplits) {
-    chunk = (max_len + kMaxSplits - 1) / kMaxSplits;
-    chunk = (chunk + least - 1) / least * least;
-    splits = (max_len + chunk - 1) / chunk;
-  }
-  if (pl.waves && units >= kComputeUnits) splits = 1;
-  if (splits < 1) splits = 1;
+  const double keys = double(units) * max_len;
+  const long least = pl.waves ? 512 : keys >= 512.0 * 256 ? 256 : 128;
+  double want = std::max(keys / double(target), double(max_len) / kMaxSplits);
+  if (pl.waves && units >= kComputeUnits) want = max_len;
+  if (long(kv.total_q) * q_heads > kMaxWgs256) want = max_len;
+  const long chunk = std::max(1l, (long(want) + least) / least) * least;
+  const long splits = std::max(1l, (max_len + chunk - 1) / chunk);
   pl.splits = int(splits);
-  pl.chunk = chunk < (1 << 30) ? int(chunk) : 1 << 30;
+  pl.chunk = int(std::min(chunk, 1l << 30));
+  pl.wgs = units * splits;
   const size_t parts = splits > 1 ? size_t(kv.total_q) * size_t(q_heads) * size_t(splits) : 0;
   pl.ml_bytes = (parts * 8 + 255) / 256 * 256;
   pl.workspace = parts > 0 ? pl.ml_bytes + parts * size_t(kv.dim) * 4 : 0;
@@ -130,6 +129,8 @@ extern "C" w4a8_status w4a8_rope_append(const uint16_t* q_dev, int ldq, const ui
   if (q_heads < 1) return W4A8_ERR_INVALID_ARGUMENT;
   if (q_heads > W4A8_HEADS_MAX) return W4A8_ERR_UNSUPPORTED;
   if (view->batch == 0 || view->total_q == 0) return W4A8_OK;
+  if (append_block_wgs(p.kv) + append_query_wgs(p.kv, q_heads) > kMaxWgs256)
+    return W4A8_ERR_UNSUPPORTED;
   const long q_cols = long(q_heads) * p.kv.dim, kv_cols = long(p.kv.kv_heads) * p.kv.dim;
   if (!rows_ok(q_dev, ldq, q_cols) || !rows_ok(k_dev, ldk, kv_cols) ||
       !rows_ok(v_dev, ldv, kv_cols) || !rows_ok(q_out_dev, ldqo, q_cols))
@@ -174,6 +175,7 @@ extern "C" w4a8_status w4a8_paged_attention(const uint16_t* q_dev, int ldq, int 
   const long cols = long(q_heads) * p.kv.dim;
   if (!rows_ok(q_dev, ldq, cols) || !rows_ok(out_dev, ldo, cols)) return W4A8_ERR_INVALID_ARGUMENT;
   const AttnPlan pl = plan_attn(p.kv, q_heads, max_q, max_len);
+  if (pl.wgs * (pl.waves == 8 ? 2 : 1) > kMaxWgs256) return W4A8_ERR_UNSUPPORTED;
   if (pl.workspace > 0) {
     if (workspace_bytes < pl.workspace) return W4A8_ERR_BUFFER_TOO_SMALL;
     if (!workspace_dev || !aligned16(workspace_dev)) return W4A8_ERR_INVALID_ARGUMENT;

@@ -11,6 +11,10 @@
 
 namespace w4a8 {
 
+// A launch holds fewer than 2^32 threads: workgroups of 256, checked by the
+// C ABI layer before any HIP call.
+constexpr long kMaxWgs256 = (1l << 24) - 1;
+
 struct NormParams {
   const uint16_t* x;
   int ldx;
@@ -74,6 +78,18 @@ struct AppendParams {
 // disjoint); one slot per sequence where each brings one token.
 inline long append_slots(const KvArgs& kv) {
   return kv.cu_q ? (long(kv.total_q) >> kv.page_shift) + 2l * kv.batch : long(kv.batch);
+}
+// One wave per block of the cache, and one head of a query per thread, where
+// sequences bring few tokens each; else a workgroup per block and 4 heads.
+inline bool append_small(const KvArgs& kv) { return long(kv.total_q) <= 4l * kv.batch; }
+// workgroups of 256 threads: those that own blocks, then those of the queries
+inline long append_block_wgs(const KvArgs& kv) {
+  const long units = append_slots(kv) * 2 * kv.kv_heads;
+  return append_small(kv) ? (units + 3) / 4 : units;
+}
+inline long append_query_wgs(const KvArgs& kv, int q_heads) {
+  const int heads = append_small(kv) ? 1 : 4;
+  return (long(kv.total_q) * (kv.dim / 16) * ((q_heads + heads - 1) / heads) + 255) / 256;
 }
 hipError_t launch_rope_append(const AppendParams& p, hipStream_t stream);
 

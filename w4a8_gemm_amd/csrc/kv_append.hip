@@ -317,20 +317,11 @@ __global__ __launch_bounds__(kThreads) void rope_append_kernel(AppendParams p, i
 }  // namespace
 
 hipError_t launch_rope_append(const AppendParams& p, hipStream_t stream) {
-  const long slots = append_slots(p.kv);
-  const long units = slots * 2 * p.kv.kv_heads;
-  // one wave per block, and one head of a query per thread, where sequences
-  // bring few tokens each
-  const bool small = long(p.kv.total_q) <= 4l * p.kv.batch;
-  const int heads = small ? 1 : 4;
-  const long block_wgs = small ? (units + 3) / 4 : units;
-  const long parts = (p.q_heads + heads - 1) / heads;
-  const long items = long(p.kv.total_q) * (p.kv.dim / 16) * parts;
-  const long q_wgs = (items + kThreads - 1) / kThreads;
-  const long wgs = block_wgs + q_wgs;
-  if (units > 2147483647l || wgs > 2147483647l) return hipErrorInvalidValue;
+  const bool small = append_small(p.kv);
+  const long block_wgs = append_block_wgs(p.kv);
+  const long wgs = block_wgs + append_query_wgs(p.kv, p.q_heads);
   AppendParams a = p;
-  int bw = int(block_wgs), un = int(units);
+  int bw = int(block_wgs), un = int(append_slots(p.kv) * 2 * p.kv.kv_heads);
   void* args[] = {&a, &bw, &un};
   const void* fn = small ? reinterpret_cast<const void*>(&rope_append_kernel<1, 1>)
                          : reinterpret_cast<const void*>(&rope_append_kernel<4, 4>);

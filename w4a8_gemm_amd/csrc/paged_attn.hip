@@ -389,7 +389,6 @@ hipError_t launch_paged_attn(const AttnParams& p, hipStream_t stream) {
   AttnParams a = p;
   void* args[] = {&a};
   const long wgs = attn_tiles(p.kv, p.group, kAttnRows) * p.kv.kv_heads * p.splits;
-  if (wgs > 2147483647l) return hipErrorInvalidValue;
   const int dim = p.kv.dim;
   const void* fn;
   if (dim == 64) fn = reinterpret_cast<const void*>(&attn_split_kernel<64, false>);

@@ -540,9 +540,7 @@ hipError_t launch_paged_attn_tile(const AttnParams& p, int waves, hipStream_t st
   AttnParams a = p;
   void* args[] = {&a};
   const int dim = p.kv.dim;
-  if (waves != 4 && !(waves == 8 && dim > 64 && dim <= 128)) return hipErrorInvalidValue;
   const long wgs = attn_tiles(p.kv, p.group, 32 * waves) * p.kv.kv_heads * p.splits;
-  if (wgs > 2147483647l) return hipErrorInvalidValue;
   const void* fn;
   if (dim <= 64)
     fn = dim == 64 ? reinterpret_cast<const void*>(&attn_tile_kernel<64, false, 4, 2>)

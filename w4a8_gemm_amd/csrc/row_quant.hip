@@ -19,6 +19,9 @@ namespace {
 
 using namespace dev;
 
+// Rows from which 4 chunks a thread beat one.  Few rows leave compute units
+// idle, and a row's time is its loads' latency; many rows share the units,
+// and fewer waves a row spend less on the reduction.
 constexpr int kManyRows = 512;
 constexpr int kThreads = 256;      // of the kernels for long or unaligned rows
 
@@ -338,9 +341,11 @@ struct Held {
 Held held_plan(int m, int k) {
   const int n = (k + 7) / 8;
   const int most = m >= kManyRows ? 4 : 1;
-  for (int t = 256; t <= 1024; t *= 2)
-    if (n <= most * t) return {t, (n + t - 1) / t};
-  return {n <= 4096 ? 1024 : 0, (n + 1023) / 1024};
+  int t = 256;
+  while (t < 1024 && n > most * t) t *= 2;
+  // a launch holds fewer than 2^32 threads
+  if (n > 4 * t || long(m) * t >= 1l << 32) return {0, 0};
+  return {t, (n + t - 1) / t};
 }
 
 #define W4A8_HELD(kernel, h)                                                        \
