@@ -552,8 +552,8 @@ hipError_t launch_paged_attn_tile(const AttnParams& p, int waves, hipStream_t st
     fn = dim == 128 ? reinterpret_cast<const void*>(&attn_tile_kernel<128, false, 8, 2>)
                     : reinterpret_cast<const void*>(&attn_tile_kernel<128, true, 8, 2>);
   else
-    fn = dim == 128 ? reinterpret_cast<const void*>(&attn_tile_kernel<128, false, 4, 1>)
-                    : reinterpret_cast<const void*>(&attn_tile_kernel<128, true, 4, 1>);
+    fn = dim == 128 ? reinterpret_cast<const void*>(&attn_tile_kernel<128, false, 4, 2>)
+                    : reinterpret_cast<const void*>(&attn_tile_kernel<128, true, 4, 2>);
   return hipLaunchKernel(fn, dim3(unsigned(wgs)), dim3(64 * waves), args, 0, stream);
 }
 
