@@ -263,6 +263,39 @@ def test_chunks(page, heads, kv_heads, dim, window):
     check_attention(batch, q, attend(batch, q, dev, window=window, max_q=1, max_len=10), window)
 
 
+@pytest.mark.parametrize("dim,window", [(128, 0), (128, 100), (80, 0)])
+def test_chunks_that_fill_the_device(dim, window):
+    """So many row tiles that the kernel with two halves of waves is taken."""
+    dev = device()
+    log(f"wide tiles dim={dim} window={window}")
+    spans = [(300, 300), (5, 1), (330, 33), (0, 0), (257, 257), (129, 2), (64, 64), (90, 17)]
+    batch = Batch(spans, 16, 64, dim, 18)
+    q = (2 * batch.rng.standard_normal((batch.tokens, 128, dim))).astype(np.float16)
+    check_attention(batch, q, attend(batch, q, dev, window=window), window)
+
+
+@pytest.mark.parametrize("length,new,heads,kv_heads,dim,window", [
+    (3000, 30, 8, 1, 128, 0), (2500, 64, 4, 2, 64, 0), (1700, 9, 20, 1, 256, 0), (4000, 50, 4, 1, 96, 1500)])
+def test_chunk_over_a_long_sequence(length, new, heads, kv_heads, dim, window):
+    """Many rows a tile and few tiles: their keys are split and joined."""
+    dev = device()
+    log(f"chunk over a long sequence len={length} new={new} heads={heads}/{kv_heads} dim={dim}")
+    batch = Batch([(length, new), (20, 20)], 32, kv_heads, dim, 19)
+    q = (2 * batch.rng.standard_normal((batch.tokens, heads, dim))).astype(np.float16)
+    for bound in (None, length // 2):
+        check_attention(batch, q, attend(batch, q, dev, window=window, max_len=bound), window)
+
+
+def test_many_rows_joined():
+    """More split rows than the join takes four waves each for."""
+    dev = device()
+    log("many split rows")
+    lens = np.random.default_rng(20).integers(1, 1500, 80)
+    batch = Batch([(int(n), 1) for n in lens], 64, 1, 64, 21, cu=False)
+    q = (2 * batch.rng.standard_normal((80, 64, 64))).astype(np.float16)
+    check_attention(batch, q, attend(batch, q, dev))
+
+
 def test_rows_that_see_nothing():
     """Length 0, and every page of a sequence absent: zeros, not NaN."""
     dev = device()
