@@ -74,6 +74,7 @@ struct AttnPlan {
 
 constexpr long kComputeUnits = 256;
 constexpr int kMaxSplits = 256;
+constexpr long kFewPartials = 1500000;
 
 AttnPlan plan_attn(const KvArgs& kv, int q_heads, int max_q, int max_len) {
   AttnPlan pl;
@@ -87,20 +88,30 @@ AttnPlan plan_attn(const KvArgs& kv, int q_heads, int max_q, int max_len) {
   }
   const long units = attn_tiles(kv, group, pl.waves ? 32 * pl.waves : kAttnRows) * kv.kv_heads;
   // Keys per split: so many that about `target` workgroups of equal work run,
-  // at least `least`; none where row tiles alone fill the device, and none for
-  // more rows than one launch joins.
-  const long target = (pl.waves ? 2 : 24) * kComputeUnits;
+  // at least `least`; none for more rows than one launch joins.
+  //   16-row tiles: 24 workgroups a compute unit even out ragged lengths
+  //   (64 x up to 8192 keys: 6 a unit 142 us, 12 137, 24 131).
+  //   Tiles of 128 or more rows: where the partial results, 4 bytes a value
+  //   each way, are few, 3 a unit (16 x 8 tokens over 4000 keys, 0.3 M values:
+  //   81 us with 2, 56 with 3; 3 x 700 over 1400 with heads of 64, 1.4 M: 52
+  //   and 44), unless the tiles make 2 a unit by themselves.  Where they are
+  //   many, 2, and only if the tiles make less than one (512 tokens over 8000
+  //   keys, 2.1 M: 126 us with 2, 136 with 3; 2000 tokens over themselves, 8 M:
+  //   71 us unsplit, 123 split).
+  const long rows_all = long(kv.total_q) * q_heads;
+  const bool few = rows_all * kv.dim <= kFewPartials;
+  const long target = (!pl.waves ? 24 : few ? 3 : 2) * kComputeUnits;
   const double keys = double(units) * max_len;
   const long least = pl.waves ? 512 : keys >= 512.0 * 256 ? 256 : 128;
   double want = std::max(keys / double(target), double(max_len) / kMaxSplits);
-  if (pl.waves && units >= kComputeUnits) want = max_len;
-  if (long(kv.total_q) * q_heads > kMaxWgs256) want = max_len;
+  if (pl.waves && units >= (few ? 2 : 1) * kComputeUnits) want = max_len;
+  if (rows_all > kMaxWgs256) want = max_len;
   const long chunk = std::max(1l, (long(want) + least) / least) * least;
   const long splits = std::max(1l, (max_len + chunk - 1) / chunk);
   pl.splits = int(splits);
   pl.chunk = int(std::min(chunk, 1l << 30));
   pl.wgs = units * splits;
-  const size_t parts = splits > 1 ? size_t(kv.total_q) * size_t(q_heads) * size_t(splits) : 0;
+  const size_t parts = splits > 1 ? size_t(rows_all) * size_t(splits) : 0;
   pl.ml_bytes = (parts * 8 + 255) / 256 * 256;
   pl.workspace = parts > 0 ? pl.ml_bytes + parts * size_t(kv.dim) * 4 : 0;
   return pl;

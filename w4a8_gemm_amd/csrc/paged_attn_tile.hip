@@ -112,8 +112,8 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
   // heads fastest (neighbouring workgroups land on different dies, so a die
   // keeps few heads' keys in its L2); the last tiles, which see the most
   // keys, first
-  const int split = blockIdx.x % p.splits;
   const int rest = blockIdx.x / p.splits;
+  const int split = (blockIdx.x % p.splits + (rest >> 2)) % p.splits;   // turned as in paged_attn.hip
   const int head = rest % kv.kv_heads;
   const int tiles = gridDim.x / p.splits / kv.kv_heads;
   const int tile = tiles - 1 - rest / kv.kv_heads;
