@@ -79,9 +79,16 @@ struct AppendParams {
 inline long append_slots(const KvArgs& kv) {
   return kv.cu_q ? (long(kv.total_q) >> kv.page_shift) + 2l * kv.batch : long(kv.batch);
 }
-// One wave per block of the cache, and one head of a query per thread, where
-// sequences bring few tokens each; else a workgroup per block and 4 heads.
-inline bool append_small(const KvArgs& kv) { return long(kv.total_q) <= 4l * kv.batch; }
+// One wave per block of the cache, and one head of a query per thread, where a
+// block's new values are at most 128 items of 16 (two a lane): 64 x 16 tokens
+// into pages of 16 7.5 us against 12.8 with a workgroup per block, 4 x 1500
+// into pages of 16 22.3 against 27.9; beyond, a workgroup per block and 4
+// heads a thread (pages of 32 22.3 against 23.5, of 64 22.8 against 27.1).
+inline bool append_small(const KvArgs& kv) {
+  const long each = (long(kv.total_q) + kv.batch - 1) / kv.batch;
+  const long page = 1l << kv.page_shift;
+  return (each < page ? each : page) * (kv.dim / 16) <= 128;
+}
 // workgroups of 256 threads: those that own blocks, then those of the queries
 inline long append_block_wgs(const KvArgs& kv) {
   const long units = append_slots(kv) * 2 * kv.kv_heads;

@@ -12,6 +12,10 @@
 // items are 16 values: the two 8-value halves of 8 rotated pairs (positions j
 // and j + rotary/2 in the half layout, 2j and 2j + 1 in the interleaved one),
 // or 16 values that are not rotated.
+//
+// Measured: the next token of 64 sequences (32 + 8 heads of 128) 4.7 us, a
+// launch's latency; 4 prompts of up to 1500 tokens (110 MB) 24.6 us = 4.5 TB/s,
+// where a large copy reaches 5.2.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -33,8 +33,8 @@ static __device__ __forceinline__ Seq seq_of(const KvArgs& a, int b) {
   return s;
 }
 
-// The largest b with first(b) <= w, first(b) = floor(cu_q[b] * mul >> / div)
-// + per * b: the sequence that owns virtual index w; *index is w's place in it.
+// The largest b with first(b) <= w, for an ascending first: the sequence that
+// owns virtual index w; *index is w's place in it.
 // first(0) is 0 for a proper cu_q; an improper one gives some sequence in range.
 template <typename First>
 static __device__ __forceinline__ int owner(int w, int batch, First first, int* index) {

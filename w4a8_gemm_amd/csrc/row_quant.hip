@@ -7,8 +7,14 @@
 // norm's y needs the row's sum of squares.  Both come out of one reduction:
 //   y = rstd * (h * w), and rounding rstd * t is monotone in |t|, so
 //   max|y| = rstd * max|h * w| exactly as the codes see it.
+//
+// Bound by memory: rows stay in registers, so every byte moves once.  Norm of
+// 4096 x 8192 with residual (235 MB) 41 us = 5.7 TB/s, SwiGLU of 2048 x 24576
+// (252 MB) 47 us = 5.4 TB/s; a large copy reaches 5.2.  8 rows of 4096: 3.7 us,
+// a launch's latency.
 
 #include <hip/hip_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include "decoder_kernels.h"
@@ -19,9 +25,12 @@ namespace {
 
 using namespace dev;
 
-// Rows from which 4 chunks a thread beat one.  Few rows leave compute units
-// idle, and a row's time is its loads' latency; many rows share the units,
-// and fewer waves a row spend less on the reduction.
+// Rows of the norm from which up to 4 chunks a thread beat one (512 x 8192: 8.9
+// us against 9.5, 4096 x 8192: 41 against 49; 256 x 8192: 5.6 against 5.5).
+// Few rows leave compute units idle, and a row's time is its loads' latency;
+// many rows share the units, and fewer waves a row spend less on the
+// reduction.  SwiGLU, with an exponential and a reciprocal a value, takes one
+// chunk a thread for any number of rows (2048 x 14336: 27 us against 30).
 constexpr int kManyRows = 512;
 constexpr int kThreads = 256;      // of the kernels for long or unaligned rows
 
@@ -338,9 +347,9 @@ __global__ __launch_bounds__(T) void silu_mul_quant_held_kernel(SwigluParams p) 
 struct Held {
   int threads, chunks;      // threads 0: the row is too long
 };
-Held held_plan(int m, int k) {
+Held held_plan(int m, int k, int many) {
   const int n = (k + 7) / 8;
-  const int most = m >= kManyRows ? 4 : 1;
+  const int most = m >= many ? 4 : 1;
   int t = 256;
   while (t < 1024 && n > most * t) t *= 2;
   // a launch holds fewer than 2^32 threads
@@ -371,7 +380,7 @@ hipError_t launch_rms_norm_quant(const NormParams& p, hipStream_t stream) {
                    rows8(p.a8, p.lda8);
   NormParams q = p;
   void* args[] = {&q};
-  const Held held = held_plan(p.m, p.k);
+  const Held held = held_plan(p.m, p.k, kManyRows);
   if (vec && held.threads)
     return hipLaunchKernel(W4A8_HELD(rms_norm_quant_held_kernel, held), dim3(p.m),
                            dim3(held.threads), args, 0, stream);
@@ -385,7 +394,7 @@ hipError_t launch_silu_mul_quant(const SwigluParams& p, hipStream_t stream) {
                    rows8(p.a8, p.lda8);
   SwigluParams q = p;
   void* args[] = {&q};
-  const Held held = held_plan(p.m, p.k);
+  const Held held = held_plan(p.m, p.k, INT_MAX);
   if (vec && held.threads)
     return hipLaunchKernel(W4A8_HELD(silu_mul_quant_held_kernel, held), dim3(p.m),
                            dim3(held.threads), args, 0, stream);
