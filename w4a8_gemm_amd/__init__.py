@@ -9,6 +9,9 @@ the library has not been built, importing this module raises.
     wdev  = to_device(blob)                  # one copy to HBM
     a8, s_a = quant_act(a)                   # per-token int8 (GPU)
     y     = gemm(a8, s_a, wdev, n, k, g)     # W4A8 GEMM (GPU)
+
+Between the linears of a decoder: rms_norm_quant, silu_mul_quant, and a paged
+int8 KV cache (kv_cache, rope_table, rope_append, paged_attention).
 """
 from __future__ import annotations
 
