@@ -286,6 +286,28 @@ def test_chunk_over_a_long_sequence(length, new, heads, kv_heads, dim, window):
         check_attention(batch, q, attend(batch, q, dev, window=window, max_len=bound), window)
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim", [(20, 1, 64), (20, 1, 128), (34, 2, 96), (18, 1, 256), (68, 4, 32)])
+@pytest.mark.parametrize("window", [0, 150])
+def test_tiles_with_waves_that_have_no_rows(heads, kv_heads, dim, window):
+    """One wave of four makes scores of the first key tile, the others go
+    straight to staging later tiles' keys; or, under a window, waves start at
+    different tiles.  Every tile's keys are of another size, so that keys of
+    a later tile in the place of an earlier one's would show."""
+    dev = device()
+    spans = [(n, 1) for n in (20, 64, 65, 129, 193, 257, 400, 640, 90, 310)] + [(500, 9), (330, 40), (260, 13)]
+    for cu in (True, False):
+        log(f"waves without rows heads={heads}/{kv_heads} dim={dim} window={window} cu={cu}")
+        batch = Batch(spans if cu else spans[:10], 16, kv_heads, dim, 22, cu=cu)
+        for b in range(len(batch.spans)):
+            for i, at in enumerate(batch.table[b]):
+                if at >= 0:
+                    batch.scale[at, 0] *= np.float16((1.0, 0.25, 3.0)[i // 4 % 3])
+        q = (2 * batch.rng.standard_normal((batch.tokens, heads, dim))).astype(np.float16)
+        # unsplit, and split over the keys
+        check_attention(batch, q, attend(batch, q, dev, window=window, max_q=40, max_len=64), window)
+        check_attention(batch, q, attend(batch, q, dev, window=window, max_q=40, max_len=4096), window)
+
+
 def test_many_rows_joined():
     """More split rows than the join takes four waves each for."""
     dev = device()

@@ -435,9 +435,18 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
   // products run beside the other's softmax; a barrier after every stretch
   // keeps them in step.
   // At tile t's matrix stretch keys of t + 2 and values of t + 1 are staged,
-  // into the buffers of t's keys and t - 1's values: both halves have then
-  // read those for the last time, and the barrier after the second half's
-  // stretch comes before anyone reads the new ones.
+  // into the buffers of t's keys and t - 1's values, which every wave must
+  // have read for the last time:
+  //   t's keys are read by the scores of t, in the matrix stretch of t - 1 or,
+  //   for the first tile, before the loop; t - 1's values in the stretch of t - 1.
+  //   With 8 waves the barriers around the softmax of t lie between (a half's
+  //   stretch t - 1 ends two barriers before its stretch t, the other half's
+  //   one before it).  With 4 waves the barrier at the end of an iteration
+  //   does for t > first, and one of its own after the first scores for
+  //   t = first: a wave without rows, or whose window starts later, has no scores
+  //   to make there and would reach its staging while others still read.
+  // The barrier after the (second half's) stretch comes before anyone reads
+  // what was staged.
   constexpr bool kTwoHalves = NW == 8;
   const bool behind = kTwoHalves && wave >= NW / 2;
   if (first < last) {
@@ -463,7 +472,7 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
   lds_barrier();
   if (w_first == first && w_first < w_last)
     products(0, 0, scores_begin, scores_end, [](int) {});
-  if (behind) lds_barrier();
+  if (!kTwoHalves || behind) lds_barrier();
   int buf = 0;
   for (int tl = first; tl < last; ++tl) {
     // asked for first: the barriers wait for scalar loads as well
