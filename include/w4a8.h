@@ -459,8 +459,10 @@ w4a8_status w4a8_rope_append(const uint16_t* q_dev, int ldq, const uint16_t* k_d
  *                   q_heads, max_q, max_len) bytes (host only; pointers in the view
  *                   are only checked for null); may be NULL when that is 0.
  *                   No initialisation; calls in flight at once need one each.
- * Scores, softmax statistics and sums are fp32; the softmax weights enter the
- * second product as fp16.  Results do not depend on scheduling (no atomics).
+ * Scores, softmax statistics and sums are fp32.  The softmax weights, times
+ * their page's value scale, enter the second product as fp16: rounded to 11
+ * bits, or to steps of 2^-34 of the row's largest where those are coarser.
+ * Results do not depend on scheduling (no atomics).
  * batch or total_q of 0 is a no-op.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED (as w4a8_rope_append; q_heads not a
  * multiple of kv_heads; more row tiles than one launch holds),

@@ -308,6 +308,46 @@ def test_tiles_with_waves_that_have_no_rows(heads, kv_heads, dim, window):
         check_attention(batch, q, attend(batch, q, dev, window=window, max_q=40, max_len=4096), window)
 
 
+@pytest.mark.parametrize("light", [0.0, 2.0 ** -24, 2.0 ** -12])
+@pytest.mark.parametrize("spans,heads,kv_heads,dim,cu", [
+    ([(600, 1), (600, 1), (70, 1)], 8, 2, 128, False),                  # one row tile of 16
+    ([(600, 40), (600, 64), (70, 9)], 8, 2, 128, True),                 # 4 waves
+    ([(600, 40), (600, 64), (70, 9)], 4, 2, 64, True),
+    ([(600, 40), (600, 17), (70, 9)], 4, 2, 256, True),
+    ([(600, 300), (400, 300), (300, 257), (64, 17)], 128, 64, 128, True),   # 8 waves
+])
+def test_mass_in_pages_of_small_values(spans, heads, kv_heads, dim, cu, light):
+    """One key of large values, at score 0, beside hundreds at score -8 whose
+    pages' values are 0 or tiny: these carry a sixth of the softmax's sum,
+    but, with the value scale in it, less than 2^-24 of the largest weight.
+
+    Beyond the reference's bound, such a weight is rounded at fp16's smallest
+    steps: the largest weight is at least 2^10 there, half a step is 2^-25, so a
+    key's product is off by 2^-35 * 127 of the largest weight."""
+    dev = device()
+    log(f"small values heads={heads}/{kv_heads} dim={dim} light={light}")
+    page = 16
+    batch = Batch(spans, page, kv_heads, dim, 23, cu=cu)
+    # score of a key: the mean of the query's values, times code * scale
+    batch.cache[:, 0] = -100
+    batch.scale[:, 0] = 0.08
+    batch.scale[:, 1] = light
+    if light == 0:
+        batch.cache[:, 1] = 0
+    for b, (length, _) in enumerate(spans):
+        at = batch.table[b, 0 if b % 2 == 0 else (length // 2) // page]   # before and after most others
+        batch.scale[at, 0], batch.scale[at, 1] = 0.3, 1.0
+        batch.cache[at, 0, :, 5] = 0
+        batch.cache[at, 1] = batch.rng.integers(64, 128, batch.cache[at, 1].shape)
+    q = np.broadcast_to(batch.rng.choice([0.75, 1.0, 1.25], (batch.tokens, heads, 1)), (batch.tokens, heads, dim))
+    q = q.astype(np.float16)
+    o = attend(batch, q, dev, scale=1.0 / dim)
+    want, bound = dref.attention(q, batch.cache, batch.scale, batch.table, batch.lens, batch.cu, 1.0 / dim)
+    err = np.abs(o.astype(np.float64) - want)
+    bound = bound + 600 * 127 * 2.0 ** -35
+    assert (err <= bound).all(), (np.unravel_index((err - bound).argmax(), err.shape), (err / bound).max())
+
+
 def test_many_rows_joined():
     """More split rows than the join takes four waves each for."""
     dev = device()

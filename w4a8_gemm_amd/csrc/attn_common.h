@@ -7,7 +7,9 @@
 // page's value scale sv joins the softmax weight in the exponent:
 //   sum_t p_t sv_t code_t  with  p_t sv_t = exp2(score_t + log2 sv_t - M),
 // M the running maximum of score + log2 sv.  The weights' own sum divides
-// sv out again, page by page, in fp32.
+// sv out again, page by page, in fp32, from the weights before they are rounded
+// to fp16: a page of small values has weights far below the others', whose
+// few bits do for its values but not for its part of the sum.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>

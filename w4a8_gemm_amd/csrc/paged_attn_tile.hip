@@ -397,12 +397,13 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[n >> 1][8 * (n & 1) + i], g[n].sk, c));
+          // summed before the rounding: a weight carries its page's value
+          // scale, and where that is far below the others' the rounded weight
+          // has few bits or none, while its part of the sum, once the scale is
+          // divided out, may be the largest
+          sum[n] += e;
           pt[n][i] = static_cast<_Float16>(e);
         }
-        // the sum of the rounded weights, as the values get them
-#pragma unroll
-        for (int i = 0; i < 8; i += 2)
-          sum[n] = __builtin_amdgcn_fdot2(half2_t{pt[n][i], pt[n][i + 1]}, half2_t{(_Float16)1.0f, (_Float16)1.0f}, sum[n], false);
       }
     };
     weights();
