@@ -93,3 +93,54 @@ def test_two_streams_same_weights_different_rows():
     torch.cuda.synchronize()
     for y, want in zip(outs, alone):
         assert torch.equal(y, want)
+
+
+def test_own_buffers_on_a_side_stream():
+    """Calls with stream= that allocate their own workspace and outputs, while
+    the current stream still works in workspaces and outputs that it has
+    freed; results read on the current stream after waiting for the other."""
+    import torch
+    dev = torch.device("cuda:0")
+    rng = np.random.default_rng(90)
+    heads, kvh, dim, page, length, batch = 32, 8, 128, 64, 6000, 4
+    pages = -(-length // page)
+    half = lambda *shape: torch.from_numpy(rng.standard_normal(shape).astype(np.float16)).to(dev)
+    cache, scale = w4.kv_cache(batch * pages, kvh, dim, page, dev)
+    cache.copy_(torch.from_numpy(rng.integers(-127, 128, cache.shape).astype(np.int8)))
+    scale.fill_(0.01)
+    table = torch.arange(batch * pages, dtype=torch.int32, device=dev).view(batch, pages)
+    lens = torch.full((batch,), length, dtype=torch.int32, device=dev)
+    q, k, x = half(batch, heads, dim), half(batch, kvh, dim), half(64, 4096)
+    weight = half(4096)
+    turn = w4.rope_table(length, dim, device=dev)
+    m, n, kk, g = LAYERS[2]
+    layer = make_layer(2, m, n, kk, g, dev)
+
+    def everything(**kw):
+        out = [w4.rope_append(q, k, k, turn, cache, scale, table, lens, **kw)]
+        out.append(w4.paged_attention(out[0], cache, scale, table, lens, **kw))
+        out += w4.rms_norm_quant(x, weight, residual=x, **kw)
+        out += w4.silu_mul_quant(x, **kw)
+        out += w4.linear(layer["a"], layer["w"], n, kk, g, **kw)
+        return out
+
+    log("side stream: alone")
+    everything()          # the page written last has its scale from here on
+    want = everything()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream(device=dev)
+    for rep in range(3):
+        log(f"side stream: pass {rep}")
+        for _ in range(10):
+            everything()                       # queued here, its buffers free at once
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(10):
+            everything()
+        got = everything(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        copies = [t.clone() for t in got]
+        del got
+        everything(stream=side)                # may take the freed results' memory
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(copies, want)):
+            assert torch.equal(a, b), (rep, i)

@@ -10,6 +10,9 @@ the library has not been built, importing this module raises.
     a8, s_a = quant_act(a)                   # per-token int8 (GPU)
     y     = gemm(a8, s_a, wdev, n, k, g)     # W4A8 GEMM (GPU)
 
+GPU calls take stream=, a torch.cuda.Stream to launch on (default: the current
+one); that the inputs are ready there is the caller's to arrange.
+
 Between the linears of a decoder: rms_norm_quant, silu_mul_quant, and a paged
 int8 KV cache (kv_cache, rope_table, rope_append, paged_attention).
 """
@@ -177,19 +180,31 @@ def _torch():
     return sys.modules["torch"]      # imported by _load()
 
 
-def _stream_ptr(stream=None) -> int:
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
-
-
 def _stream_of(t, stream=None) -> int:
     """The given stream, or the current one of t's device."""
     if stream is not None:
         return int(stream.cuda_stream)
-    # the raw handle where torch offers it: a Stream object takes 2.6 us to make
-    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
-    return raw(t.device.index) if raw else _stream_ptr()
+    # the raw handle where torch offers it: a Stream object takes 2.9 us to make
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(t.device.index) if raw else int(torch.cuda.current_stream(t.device).cuda_stream)
+
+
+def _empty(shape, dtype, device, stream, returned=True):
+    """A buffer for a call that launches on `stream` (None: the current one),
+    from that stream's pool: memory of the current stream may still be in use
+    by work queued there.  One that is returned is marked as used by the current
+    stream too, where it will be read, so that its memory is not given out again
+    before that is done."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(caller)
+    return t
 
 
 def to_device(blob: np.ndarray, device="cuda"):
@@ -204,11 +219,11 @@ def quant_act(a, a8=None, s_a=None, stream=None):
     assert a.dtype == torch.float16 and a.is_cuda and a.dim() == 2 and a.stride(1) == 1
     m, k = a.shape
     if a8 is None:
-        a8 = torch.empty((m, k), dtype=torch.int8, device=a.device)
+        a8 = _empty((m, k), torch.int8, a.device, stream)
     if s_a is None:
-        s_a = torch.empty((m,), dtype=torch.float16, device=a.device)
+        s_a = _empty((m,), torch.float16, a.device, stream)
     _check(lib.w4a8_quant_act(a.data_ptr(), m, k, a.stride(0), a8.data_ptr(), a8.stride(0),
-                              s_a.data_ptr(), _stream_ptr(stream)), "w4a8_quant_act")
+                              s_a.data_ptr(), _stream_of(a, stream)), "w4a8_quant_act")
     return a8, s_a
 
 
@@ -220,12 +235,12 @@ def quant_act_static(a, scale, a8=None, s_a=None, stream=None):
     assert a.dtype == torch.float16 and a.is_cuda and a.dim() == 2 and a.stride(1) == 1
     m, k = a.shape
     if a8 is None:
-        a8 = torch.empty((m, k), dtype=torch.int8, device=a.device)
+        a8 = _empty((m, k), torch.int8, a.device, stream)
     if s_a is None:
-        s_a = torch.empty((m,), dtype=torch.float16, device=a.device)
+        s_a = _empty((m,), torch.float16, a.device, stream)
     bits = int(np.array([scale], dtype=np.float16).view(np.uint16)[0])
     _check(lib.w4a8_quant_act_static(a.data_ptr(), m, k, a.stride(0), bits, a8.data_ptr(),
-                                     a8.stride(0), s_a.data_ptr(), _stream_ptr(stream)),
+                                     a8.stride(0), s_a.data_ptr(), _stream_of(a, stream)),
            "w4a8_quant_act_static")
     return a8, s_a
 
@@ -238,23 +253,23 @@ def gemm(a8, s_a, blob_dev, n: int, k: int, g: int, y=None, acc=None, want_acc=F
     m = a8.shape[0]
     assert a8.dtype == torch.int8 and a8.is_cuda and a8.stride(1) == 1
     if y is None:
-        y = torch.empty((m, n), dtype=torch.float16, device=a8.device)
+        y = _empty((m, n), torch.float16, a8.device, stream)
     if want_acc and acc is None:
-        acc = torch.empty((m, n), dtype=torch.int32, device=a8.device)
+        acc = _empty((m, n), torch.int32, a8.device, stream)
     opts = None
     if variant or k_split or n_tiles or m_tiles or stages or row_groups or slices:
         opts = GemmOpts(variant, k_split, n_tiles, m_tiles, stages, row_groups, slices)
     ws_need = int(lib.w4a8_gemm_workspace_size(m, n, k, g,
                                                ctypes.byref(opts) if opts is not None else None))
     if ws_need and workspace is None:
-        workspace = torch.empty(ws_need, dtype=torch.uint8, device=a8.device)
+        workspace = _empty(ws_need, torch.uint8, a8.device, stream, returned=False)
     st = lib.w4a8_gemm(a8.data_ptr(), a8.stride(0), s_a.data_ptr(), m, blob_dev.data_ptr(), n, k,
                        g, y.data_ptr(), y.stride(0),
                        acc.data_ptr() if acc is not None else None,
                        acc.stride(0) if acc is not None else 0,
                        workspace.data_ptr() if workspace is not None else None,
                        workspace.numel() if workspace is not None else 0,
-                       ctypes.byref(opts) if opts is not None else None, _stream_ptr(stream))
+                       ctypes.byref(opts) if opts is not None else None, _stream_of(a8, stream))
     _check(st, "w4a8_gemm")
     return (y, acc) if acc is not None else y
 
@@ -273,7 +288,7 @@ def gemm_noalloc(a8, s_a, blob_dev, n: int, k: int, g: int, y, acc=None, slices:
                                acc.data_ptr() if acc is not None else None,
                                acc.stride(0) if acc is not None else 0,
                                ctypes.byref(opts) if opts is not None else None,
-                               _stream_ptr(stream))
+                               _stream_of(a8, stream))
     _check(st, "w4a8_gemm_noalloc")
     return (y, acc) if acc is not None else y
 
@@ -288,13 +303,13 @@ def linear(a, blob_dev, n: int, k: int, g: int, y=None, a8=None, s_a=None, acc=N
     assert a.dtype == torch.float16 and a.is_cuda and a.dim() == 2 and a.stride(1) == 1
     m = a.shape[0]
     if y is None:
-        y = torch.empty((m, n), dtype=torch.float16, device=a.device)
+        y = _empty((m, n), torch.float16, a.device, stream)
     if a8 is None:
-        a8 = torch.empty((m, k), dtype=torch.int8, device=a.device)
+        a8 = _empty((m, k), torch.int8, a.device, stream)
     if s_a is None:
-        s_a = torch.empty((m,), dtype=torch.float16, device=a.device)
+        s_a = _empty((m,), torch.float16, a.device, stream)
     if want_acc and acc is None:
-        acc = torch.empty((m, n), dtype=torch.int32, device=a.device)
+        acc = _empty((m, n), torch.int32, a.device, stream)
     opts = None
     if variant or k_split or n_tiles or m_tiles or stages or row_groups or slices or workgroups:
         opts = GemmOpts(variant, k_split, n_tiles, m_tiles, stages, row_groups, slices, workgroups)
@@ -302,14 +317,14 @@ def linear(a, blob_dev, n: int, k: int, g: int, y=None, a8=None, s_a=None, acc=N
     ws_need = 0 if variant == 3 else int(lib.w4a8_gemm_workspace_size(
         m, n, k, g, ctypes.byref(ws_opts) if ws_opts is not None else None))
     if ws_need and workspace is None:
-        workspace = torch.empty(ws_need, dtype=torch.uint8, device=a.device)
+        workspace = _empty(ws_need, torch.uint8, a.device, stream, returned=False)
     st = lib.w4a8_linear(a.data_ptr(), a.stride(0), m, k, blob_dev.data_ptr(), n, g,
                          y.data_ptr(), y.stride(0), a8.data_ptr(), a8.stride(0), s_a.data_ptr(),
                          acc.data_ptr() if acc is not None else None,
                          acc.stride(0) if acc is not None else 0,
                          workspace.data_ptr() if workspace is not None else None,
                          workspace.numel() if workspace is not None else 0,
-                         ctypes.byref(opts) if opts is not None else None, _stream_ptr(stream))
+                         ctypes.byref(opts) if opts is not None else None, _stream_of(a, stream))
     _check(st, "w4a8_linear")
     return (y, a8, s_a, acc) if acc is not None else (y, a8, s_a)
 
@@ -321,13 +336,13 @@ def w4a16(a, blob_dev, n: int, k: int, g: int, y=None, variant: int = 0, k_split
     assert a.dtype == torch.float16 and a.is_cuda and a.dim() == 2 and a.stride(1) == 1
     m = a.shape[0]
     if y is None:
-        y = torch.empty((m, n), dtype=torch.float16, device=a.device)
+        y = _empty((m, n), torch.float16, a.device, stream)
     opts = None
     if variant or k_split or n_tiles:
         opts = GemmOpts(variant, k_split, n_tiles)
     _check(lib.w4a16_gemm(a.data_ptr(), a.stride(0), m, k, blob_dev.data_ptr(), n, g,
                           y.data_ptr(), y.stride(0),
-                          ctypes.byref(opts) if opts is not None else None, _stream_ptr(stream)),
+                          ctypes.byref(opts) if opts is not None else None, _stream_of(a, stream)),
            "w4a16_gemm")
     return y
 
@@ -340,15 +355,15 @@ def _rows(name, t, dtype, m=None, k=None):
         raise ValueError(f"{name}: expected shape ({m}, {k}), got {tuple(t.shape)}")
 
 
-def _int8_out(m, k, a8, s_a, device):
+def _int8_out(m, k, a8, s_a, device, stream):
     """The outputs of a per-token quantizer, allocated where not given."""
     torch = _torch()
     if a8 is None:
-        a8 = torch.empty((m, k), dtype=torch.int8, device=device)
+        a8 = _empty((m, k), torch.int8, device, stream)
     else:
         _rows("a8", a8, torch.int8, m, k)
     if s_a is None:
-        s_a = torch.empty((m,), dtype=torch.float16, device=device)
+        s_a = _empty((m,), torch.float16, device, stream)
     elif (s_a.dtype is not torch.float16 or not s_a.is_cuda or s_a.shape != (m,)
           or not s_a.is_contiguous()):
         raise ValueError(f"s_a: expected a contiguous float16 CUDA tensor of {m} values")
@@ -374,10 +389,10 @@ def rms_norm_quant(x, weight, eps: float = 1e-5, residual=None, h=None, a8=None,
     if residual is not None:
         _rows("residual", residual, torch.float16, m, k)
         if h is None:
-            h = torch.empty((m, k), dtype=torch.float16, device=x.device)
+            h = _empty((m, k), torch.float16, x.device, stream)
     if h is not None:
         _rows("h", h, torch.float16, m, k)
-    a8, s_a = _int8_out(m, k, a8, s_a, x.device)
+    a8, s_a = _int8_out(m, k, a8, s_a, x.device, stream)
     _check(lib.w4a8_rms_norm_quant(
         x.data_ptr(), _ld(x), residual.data_ptr() if residual is not None else None,
         _ld(residual) if residual is not None else 0, weight.data_ptr(), eps, m, k,
@@ -400,7 +415,7 @@ def silu_mul_quant(gate, up=None, a8=None, s_a=None, stream=None):
         m, k = gate.shape
         _rows("up", up, torch.float16, m, k)
         up_ptr, ldu = up.data_ptr(), _ld(up)
-    a8, s_a = _int8_out(m, k, a8, s_a, gate.device)
+    a8, s_a = _int8_out(m, k, a8, s_a, gate.device, stream)
     _check(lib.w4a8_silu_mul_quant(gate.data_ptr(), _ld(gate), up_ptr, ldu, m, k, a8.data_ptr(),
                                    _ld(a8), s_a.data_ptr(), _stream_of(gate, stream)),
            "w4a8_silu_mul_quant")
@@ -520,7 +535,7 @@ def rope_append(q, k, v, cos_sin, cache, scale, block_table, seq_lens, cu_q=None
             raise ValueError("cos_sin: expected a contiguous float32 CUDA tensor [max_pos, rotary_dim]")
         max_pos, rotary = cos_sin.shape
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=torch.float16, device=q.device)
+        out = _empty((tokens, heads, dim), torch.float16, q.device, stream)
     _check(lib.w4a8_rope_append(
         q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, heads,
         cos_sin.data_ptr() if cos_sin is not None else None, rotary, max_pos, int(interleaved),
@@ -541,16 +556,14 @@ def paged_attention(q, cache, scale_kv, block_table, seq_lens, cu_q=None, max_q:
     view = _kv_view(cache, scale_kv, block_table, seq_lens, cu_q, tokens)
     ldq = _heads("q", q, tokens, None, view.head_dim)
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=torch.float16, device=q.device)
+        out = _empty((tokens, heads, dim), torch.float16, q.device, stream)
     if max_len is None:
         max_len = view.max_pages * view.page_size
     if max_q is None:
         max_q = 1 if cu_q is None else tokens
     need = lib.w4a8_paged_attention_workspace_size(ctypes.byref(view), heads, max_q, max_len)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None:
-            workspace.record_stream(stream)     # freed here, in use there
+        workspace = _empty(need, torch.uint8, q.device, stream, returned=False)
     _check(lib.w4a8_paged_attention(
         q.data_ptr(), ldq, heads, ctypes.byref(view), max_q, max_len,
         dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
@@ -568,4 +581,4 @@ def read_probe(buf, offset: int, nbytes: int, workgroups: int, sink, stream=None
     assert buf.is_cuda and 0 <= offset and offset + nbytes <= buf.numel() * buf.element_size()
     assert sink.numel() >= workgroups
     _check(lib.w4a8_read_probe(buf.data_ptr() + offset, nbytes, workgroups, sink.data_ptr(),
-                               _stream_ptr(stream)), "w4a8_read_probe")
+                               _stream_of(buf, stream)), "w4a8_read_probe")
