@@ -28,7 +28,8 @@
  *   - Pointers named *_dev are device (HBM) pointers; all others are host.
  *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).
  *     GPU entry points only enqueue work: they do not synchronize, allocate,
- *     free, or keep state between calls.  The caller owns every buffer.
+ *     free, or keep state between calls.  The caller owns every buffer.  They
+ *     launch on the current device, which must be the buffers' and the stream's.
  *   - Arguments are validated on the host before any HIP call.  A rejected
  *     call returns an error status and touches no memory.  A failed kernel
  *     launch returns W4A8_ERR_DEVICE; faults inside a kernel surface at the

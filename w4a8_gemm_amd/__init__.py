@@ -10,8 +10,9 @@ the library has not been built, importing this module raises.
     a8, s_a = quant_act(a)                   # per-token int8 (GPU)
     y     = gemm(a8, s_a, wdev, n, k, g)     # W4A8 GEMM (GPU)
 
-GPU calls take stream=, a torch.cuda.Stream to launch on (default: the current
-one); that the inputs are ready there is the caller's to arrange.
+GPU calls run on the device of their tensors, all on one, and take stream=, a
+torch.cuda.Stream of it to launch on (default: the current one); that the inputs
+are ready there is the caller's to arrange.
 
 Between the linears of a decoder: rms_norm_quant, silu_mul_quant, and a paged
 int8 KV cache (kv_cache, rope_table, rope_append, paged_attention).
@@ -19,11 +20,18 @@ int8 KV cache (kv_cache, rope_table, rope_append, paged_attention).
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import re
-import sys
 
 import numpy as np
+# torch is imported before the library is loaded: it carries its own HIP runtime
+# (same soname as the system one).  Loading it first makes the library's
+# libamdhip64 dependency resolve to that already-loaded runtime, so torch
+# allocations, torch streams and this library's kernels share one HIP runtime
+# in the process.
+import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libw4a8.so")
@@ -70,12 +78,6 @@ class KvView(ctypes.Structure):
 
 
 def _load():
-    # torch is imported first on purpose: it carries its own HIP runtime
-    # (same soname as the system one).  Loading it first makes the library's
-    # libamdhip64 dependency resolve to that already-loaded runtime, so torch
-    # allocations, torch streams and this library's kernels share one HIP
-    # runtime in the process.
-    import torch  # noqa: F401
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
                           "`python w4a8_gemm_amd/build.py` (or __graft_entry__.build())")
@@ -176,18 +178,35 @@ def unpack(blob: np.ndarray) -> dict:
 
 
 # ------------------------------------------------------------------ device side
-def _torch():
-    return sys.modules["torch"]      # imported by _load()
-
-
 def _stream_of(t, stream=None) -> int:
     """The given stream, or the current one of t's device."""
     if stream is not None:
         return int(stream.cuda_stream)
     # the raw handle where torch offers it: a Stream object takes 2.9 us to make
-    torch = _torch()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return raw(t.device.index) if raw else int(torch.cuda.current_stream(t.device).cuda_stream)
+
+
+def _on_device(fn):
+    """Runs fn(t, ...) with the device of its first tensor current, since that is
+    where a launch goes, and refuses a stream of another device."""
+    params = list(inspect.signature(fn).parameters)
+    at = params.index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        index = (args[0] if args else kw[params[0]]).get_device()
+        if index < 0:
+            return fn(*args, **kw)          # fn refuses it
+        cuda = torch.cuda
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"stream: expected one of cuda:{index}, got one of {stream.device}")
+        if index == cuda.current_device():
+            return fn(*args, **kw)
+        with cuda.device(index):
+            return fn(*args, **kw)
+    return call
 
 
 def _empty(shape, dtype, device, stream, returned=True):
@@ -196,7 +215,6 @@ def _empty(shape, dtype, device, stream, returned=True):
     by work queued there.  One that is returned is marked as used by the current
     stream too, where it will be read, so that its memory is not given out again
     before that is done."""
-    torch = _torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     caller = torch.cuda.current_stream(device)
@@ -209,13 +227,12 @@ def _empty(shape, dtype, device, stream, returned=True):
 
 def to_device(blob: np.ndarray, device="cuda"):
     """Copy a packed blob to device memory (a uint8 torch tensor)."""
-    torch = _torch()
     return torch.from_numpy(blob).to(device)
 
 
+@_on_device
 def quant_act(a, a8=None, s_a=None, stream=None):
     """Per-token int8 quantization of an M x K float16 CUDA tensor."""
-    torch = _torch()
     assert a.dtype == torch.float16 and a.is_cuda and a.dim() == 2 and a.stride(1) == 1
     m, k = a.shape
     if a8 is None:
@@ -227,11 +244,10 @@ def quant_act(a, a8=None, s_a=None, stream=None):
     return a8, s_a
 
 
+@_on_device
 def quant_act_static(a, scale, a8=None, s_a=None, stream=None):
     """Int8 quantization of an M x K float16 CUDA tensor with one static
     fp16 scale; s_a is filled with the scale for every row."""
-    import numpy as np
-    torch = _torch()
     assert a.dtype == torch.float16 and a.is_cuda and a.dim() == 2 and a.stride(1) == 1
     m, k = a.shape
     if a8 is None:
@@ -245,11 +261,11 @@ def quant_act_static(a, scale, a8=None, s_a=None, stream=None):
     return a8, s_a
 
 
+@_on_device
 def gemm(a8, s_a, blob_dev, n: int, k: int, g: int, y=None, acc=None, want_acc=False,
          variant: int = 0, k_split: int = 0, n_tiles: int = 0, m_tiles: int = 0,
          stages: int = 0, row_groups: int = 0, slices: int = 0, workspace=None, stream=None):
     """Y = fp16(s_a * s1 * (A8 @ W8^.T)); returns y (and the int32 acc if asked)."""
-    torch = _torch()
     m = a8.shape[0]
     assert a8.dtype == torch.int8 and a8.is_cuda and a8.stride(1) == 1
     if y is None:
@@ -274,12 +290,12 @@ def gemm(a8, s_a, blob_dev, n: int, k: int, g: int, y=None, acc=None, want_acc=F
     return (y, acc) if acc is not None else y
 
 
+@_on_device
 def gemm_noalloc(a8, s_a, blob_dev, n: int, k: int, g: int, y, acc=None, slices: int = 0,
                  stream=None):
     """w4a8_gemm_noalloc: the GEMM with no workspace argument (a K split keeps
     its partial sums in the library's static device scratch).  y (and acc,
     if given) must be preallocated; nothing is allocated here."""
-    torch = _torch()
     m = a8.shape[0]
     assert a8.dtype == torch.int8 and a8.is_cuda and a8.stride(1) == 1
     opts = GemmOpts(0, 0, 0, 0, 0, 0, slices) if slices else None
@@ -293,13 +309,13 @@ def gemm_noalloc(a8, s_a, blob_dev, n: int, k: int, g: int, y, acc=None, slices:
     return (y, acc) if acc is not None else y
 
 
+@_on_device
 def linear(a, blob_dev, n: int, k: int, g: int, y=None, a8=None, s_a=None, acc=None,
            want_acc=False, variant: int = 0, k_split: int = 0, n_tiles: int = 0,
            m_tiles: int = 0, stages: int = 0, row_groups: int = 0, slices: int = 0,
            workgroups: int = 0, workspace=None, stream=None):
     """The whole layer from fp16 activations (fused for small M); returns
     (y, a8, s_a) or (y, a8, s_a, acc)."""
-    torch = _torch()
     assert a.dtype == torch.float16 and a.is_cuda and a.dim() == 2 and a.stride(1) == 1
     m = a.shape[0]
     if y is None:
@@ -329,10 +345,10 @@ def linear(a, blob_dev, n: int, k: int, g: int, y=None, a8=None, s_a=None, acc=N
     return (y, a8, s_a, acc) if acc is not None else (y, a8, s_a)
 
 
+@_on_device
 def w4a16(a, blob_dev, n: int, k: int, g: int, y=None, variant: int = 0, k_split: int = 0,
           n_tiles: int = 0, stream=None):
     """W4A16 comparison GEMM on the same blob: fp16 A times fp16-decoded weights."""
-    torch = _torch()
     assert a.dtype == torch.float16 and a.is_cuda and a.dim() == 2 and a.stride(1) == 1
     m = a.shape[0]
     if y is None:
@@ -347,26 +363,38 @@ def w4a16(a, blob_dev, n: int, k: int, g: int, y=None, variant: int = 0, k_split
     return y
 
 
-def _rows(name, t, dtype, m=None, k=None):
-    """Check a 2-D CUDA tensor whose rows are contiguous."""
-    if t.dtype is not dtype or not t.is_cuda or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+def _elsewhere(name, t, dev):
+    return ValueError(f"{name}: expected a CUDA tensor on device {dev}, got one on {t.device}")
+
+
+def _rows(name, t, dtype, dev, m=None, k=None):
+    """Check a 2-D tensor on CUDA device `dev` whose rows are contiguous."""
+    if t.dtype is not dtype or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
         raise ValueError(f"{name}: expected a 2-D {dtype} CUDA tensor with contiguous rows")
-    if m is not None and (t.shape[0] != m or t.shape[1] != k):
+    if t.get_device() != dev or dev < 0:
+        raise _elsewhere(name, t, dev)
+    if m is not None and t.shape != (m, k):
         raise ValueError(f"{name}: expected shape ({m}, {k}), got {tuple(t.shape)}")
 
 
-def _int8_out(m, k, a8, s_a, device, stream):
+def _vector(name, t, dtype, dev, n):
+    """Check a contiguous tensor of n values on CUDA device `dev`."""
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} CUDA tensor of {n} values")
+    if t.get_device() != dev:
+        raise _elsewhere(name, t, dev)
+
+
+def _int8_out(m, k, a8, s_a, like, stream):
     """The outputs of a per-token quantizer, allocated where not given."""
-    torch = _torch()
+    if a8 is not None:
+        _rows("a8", a8, torch.int8, like.get_device(), m, k)
+    if s_a is not None:
+        _vector("s_a", s_a, torch.float16, like.get_device(), m)
     if a8 is None:
-        a8 = _empty((m, k), torch.int8, device, stream)
-    else:
-        _rows("a8", a8, torch.int8, m, k)
+        a8 = _empty((m, k), torch.int8, like.device, stream)
     if s_a is None:
-        s_a = _empty((m,), torch.float16, device, stream)
-    elif (s_a.dtype is not torch.float16 or not s_a.is_cuda or s_a.shape != (m,)
-          or not s_a.is_contiguous()):
-        raise ValueError(f"s_a: expected a contiguous float16 CUDA tensor of {m} values")
+        s_a = _empty((m,), torch.float16, like.device, stream)
     return a8, s_a
 
 
@@ -375,24 +403,23 @@ def _ld(t):
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
+@_on_device
 def rms_norm_quant(x, weight, eps: float = 1e-5, residual=None, h=None, a8=None, s_a=None,
                    stream=None):
     """h = x + residual, then the RMS norm of h quantized per token: returns
     (h, a8, s_a), a8 and s_a ready for gemm().  Without a residual h is x.
     h may be given, also as x or residual themselves (in place)."""
-    torch = _torch()
-    _rows("x", x, torch.float16)
+    dev = x.get_device()
+    _rows("x", x, torch.float16, dev)
     m, k = x.shape
-    if weight.dtype is not torch.float16 or weight.shape != (k,) or not weight.is_contiguous() \
-            or not weight.is_cuda:
-        raise ValueError(f"weight: expected a contiguous float16 CUDA tensor of {k} values")
+    _vector("weight", weight, torch.float16, dev, k)
     if residual is not None:
-        _rows("residual", residual, torch.float16, m, k)
-        if h is None:
-            h = _empty((m, k), torch.float16, x.device, stream)
+        _rows("residual", residual, torch.float16, dev, m, k)
     if h is not None:
-        _rows("h", h, torch.float16, m, k)
-    a8, s_a = _int8_out(m, k, a8, s_a, x.device, stream)
+        _rows("h", h, torch.float16, dev, m, k)
+    elif residual is not None:
+        h = _empty((m, k), torch.float16, x.device, stream)
+    a8, s_a = _int8_out(m, k, a8, s_a, x, stream)
     _check(lib.w4a8_rms_norm_quant(
         x.data_ptr(), _ld(x), residual.data_ptr() if residual is not None else None,
         _ld(residual) if residual is not None else 0, weight.data_ptr(), eps, m, k,
@@ -401,11 +428,11 @@ def rms_norm_quant(x, weight, eps: float = 1e-5, residual=None, h=None, a8=None,
     return (h if h is not None else x), a8, s_a
 
 
+@_on_device
 def silu_mul_quant(gate, up=None, a8=None, s_a=None, stream=None):
     """silu(gate) * up quantized per token: returns (a8, s_a).  With gate alone,
     its left half is the gate and its right half up (one gate-and-up output)."""
-    torch = _torch()
-    _rows("gate", gate, torch.float16)
+    _rows("gate", gate, torch.float16, gate.get_device())
     if up is None:
         if gate.shape[1] % 2:
             raise ValueError("gate: expected an even number of columns (gate and up side by side)")
@@ -413,9 +440,9 @@ def silu_mul_quant(gate, up=None, a8=None, s_a=None, stream=None):
         up_ptr, ldu = gate.data_ptr() + 2 * k, _ld(gate)
     else:
         m, k = gate.shape
-        _rows("up", up, torch.float16, m, k)
+        _rows("up", up, torch.float16, gate.get_device(), m, k)
         up_ptr, ldu = up.data_ptr(), _ld(up)
-    a8, s_a = _int8_out(m, k, a8, s_a, gate.device, stream)
+    a8, s_a = _int8_out(m, k, a8, s_a, gate, stream)
     _check(lib.w4a8_silu_mul_quant(gate.data_ptr(), _ld(gate), up_ptr, ldu, m, k, a8.data_ptr(),
                                    _ld(a8), s_a.data_ptr(), _stream_of(gate, stream)),
            "w4a8_silu_mul_quant")
@@ -425,7 +452,6 @@ def silu_mul_quant(gate, up=None, a8=None, s_a=None, stream=None):
 def kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device="cuda"):
     """A paged int8 KV cache: (cache int8 [num_pages, 2, kv_heads, page_size,
     head_dim], scale float16 [num_pages, 2, kv_heads]), [:, 0] the keys."""
-    torch = _torch()
     return (torch.zeros((num_pages, 2, kv_heads, page_size, head_dim), dtype=torch.int8, device=device),
             torch.zeros((num_pages, 2, kv_heads), dtype=torch.float16, device=device))
 
@@ -446,7 +472,6 @@ def rope_table(max_pos: int, rotary_dim: int, base: float = 10000.0, scaling: st
                        `high` times kept, a linear blend between (the scheme
                        of Llama-3.1's checkpoints)
     """
-    torch = _torch()
     if max_pos < 1 or rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rope_table: max_pos >= 1 and an even rotary_dim >= 2 are needed")
     if factor <= 0 or base <= 0 or (scaling == "bands" and not 0 < low < high):
@@ -467,29 +492,33 @@ def rope_table(max_pos: int, rotary_dim: int, base: float = 10000.0, scaling: st
     return torch.cat([angle.cos(), angle.sin()], dim=1).float().to(device)
 
 
-def _kv_view(cache, scale, block_table, seq_lens, cu_q, total_q):
-    """The C view of a cache and a batch, its tensors checked."""
-    torch = _torch()
-    if cache.dtype is not torch.int8 or cache.dim() != 5 or cache.shape[1] != 2 or not cache.is_cuda:
+def _kv_view(cache, scale, block_table, seq_lens, cu_q, q):
+    """The C view of a cache and a batch for the new tokens of q, its tensors
+    checked."""
+    total_q, dev = q.shape[0], q.get_device()
+    if cache.dtype is not torch.int8 or cache.dim() != 5 or cache.shape[1] != 2:
         raise ValueError("cache: expected an int8 CUDA tensor [pages, 2, kv_heads, page_size, head_dim]")
     pages, _, heads, page, dim = cache.shape
     if cache.stride()[1:] != (heads * page * dim, page * dim, dim, 1):
         raise ValueError("cache: the values of a page must be contiguous")
-    if scale.dtype is not torch.float16 or scale.shape != (pages, 2, heads) or not scale.is_cuda \
+    if scale.dtype is not torch.float16 or scale.shape != (pages, 2, heads) \
             or scale.stride()[1:] != (heads, 1):
         raise ValueError(f"scale: expected a float16 CUDA tensor [{pages}, 2, {heads}], "
                          "contiguous within a page")
-    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or not block_table.is_cuda \
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2 \
             or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
         raise ValueError("block_table: expected an int32 CUDA tensor [batch, pages of a sequence]")
+    if cache.get_device() != dev:
+        raise _elsewhere("cache", cache, dev)
+    if scale.get_device() != dev:
+        raise _elsewhere("scale", scale, dev)
+    if block_table.get_device() != dev:
+        raise _elsewhere("block_table", block_table, dev)
     batch, max_pages = block_table.shape
-    if seq_lens.dtype is not torch.int32 or seq_lens.shape != (batch,) or not seq_lens.is_cuda \
-            or not seq_lens.is_contiguous():
-        raise ValueError(f"seq_lens: expected a contiguous int32 CUDA tensor of {batch} values")
-    if cu_q is not None and (cu_q.dtype is not torch.int32 or cu_q.shape != (batch + 1,)
-                             or not cu_q.is_cuda or not cu_q.is_contiguous()):
-        raise ValueError(f"cu_q: expected a contiguous int32 CUDA tensor of {batch + 1} values")
-    if cu_q is None and total_q != batch:
+    _vector("seq_lens", seq_lens, torch.int32, dev, batch)
+    if cu_q is not None:
+        _vector("cu_q", cu_q, torch.int32, dev, batch + 1)
+    elif total_q != batch:
         raise ValueError(f"without cu_q each of the {batch} sequences brings one token, got {total_q}")
     return KvView(cache.data_ptr(), scale.data_ptr(),
                   cache.stride(0) if pages > 1 else 2 * heads * page * dim,
@@ -500,12 +529,13 @@ def _kv_view(cache, scale, block_table, seq_lens, cu_q, total_q):
                   batch, total_q)
 
 
-def _heads(name, t, tokens=None, heads=None, dim=None):
-    """Check a [tokens, heads, dim] float16 CUDA tensor whose rows (all heads of
-    a token) are contiguous; returns the row stride."""
-    torch = _torch()
-    if t.dtype is not torch.float16 or not t.is_cuda or t.dim() != 3:
+def _heads(name, t, dev, tokens=None, heads=None, dim=None):
+    """Check a [tokens, heads, dim] float16 tensor on CUDA device `dev` whose rows
+    (all heads of a token) are contiguous; returns the row stride."""
+    if t.dtype is not torch.float16 or t.dim() != 3:
         raise ValueError(f"{name}: expected a float16 CUDA tensor [tokens, heads, head_dim]")
+    if t.get_device() != dev or dev < 0:
+        raise _elsewhere(name, t, dev)
     n, h, d = t.shape
     if (tokens is not None and n != tokens) or (heads is not None and h != heads) \
             or (dim is not None and d != dim):
@@ -516,34 +546,37 @@ def _heads(name, t, tokens=None, heads=None, dim=None):
     return s[0] if n > 1 else max(s[0], h * d)
 
 
+@_on_device
 def rope_append(q, k, v, cos_sin, cache, scale, block_table, seq_lens, cu_q=None,
                 interleaved: bool = False, out=None, stream=None):
     """Rotate q [tokens, heads, dim] and k by position and append k and v
     [tokens, kv_heads, dim] to the paged cache; returns the rotated q (a new
     tensor, or `out`, which may be q).  cos_sin [max_pos, rotary_dim] is
     rope_table()'s, or None for no rotation.  See w4a8_rope_append."""
-    torch = _torch()
+    dev = q.get_device()
     tokens, heads, dim = q.shape
-    view = _kv_view(cache, scale, block_table, seq_lens, cu_q, tokens)
-    ldq = _heads("q", q, tokens, None, view.head_dim)
-    ldk = _heads("k", k, tokens, view.kv_heads, view.head_dim)
-    ldv = _heads("v", v, tokens, view.kv_heads, view.head_dim)
+    view = _kv_view(cache, scale, block_table, seq_lens, cu_q, q)
+    ldq = _heads("q", q, dev, tokens, None, view.head_dim)
+    ldk = _heads("k", k, dev, tokens, view.kv_heads, view.head_dim)
+    ldv = _heads("v", v, dev, tokens, view.kv_heads, view.head_dim)
     rotary = max_pos = 0
     if cos_sin is not None:
-        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_cuda \
-                or not cos_sin.is_contiguous():
+        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin: expected a contiguous float32 CUDA tensor [max_pos, rotary_dim]")
+        if cos_sin.get_device() != dev:
+            raise _elsewhere("cos_sin", cos_sin, dev)
         max_pos, rotary = cos_sin.shape
     if out is None:
         out = _empty((tokens, heads, dim), torch.float16, q.device, stream)
     _check(lib.w4a8_rope_append(
         q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, heads,
         cos_sin.data_ptr() if cos_sin is not None else None, rotary, max_pos, int(interleaved),
-        ctypes.byref(view), out.data_ptr(), _heads("out", out, tokens, heads, dim),
+        ctypes.byref(view), out.data_ptr(), _heads("out", out, dev, tokens, heads, dim),
         _stream_of(q, stream)), "w4a8_rope_append")
     return out
 
 
+@_on_device
 def paged_attention(q, cache, scale_kv, block_table, seq_lens, cu_q=None, max_q: int | None = None,
                     max_len: int | None = None, scale: float | None = None, window: int = 0, out=None, workspace=None,
                     stream=None):
@@ -551,10 +584,10 @@ def paged_attention(q, cache, scale_kv, block_table, seq_lens, cu_q=None, max_q:
     returns o like q.  max_q and max_len bound the new tokens of a sequence
     and seq_lens on the host (defaults: all of q, and what the block table
     holds); scale defaults to dim ** -0.5.  See w4a8_paged_attention."""
-    torch = _torch()
+    dev = q.get_device()
     tokens, heads, dim = q.shape
-    view = _kv_view(cache, scale_kv, block_table, seq_lens, cu_q, tokens)
-    ldq = _heads("q", q, tokens, None, view.head_dim)
+    view = _kv_view(cache, scale_kv, block_table, seq_lens, cu_q, q)
+    ldq = _heads("q", q, dev, tokens, None, view.head_dim)
     if out is None:
         out = _empty((tokens, heads, dim), torch.float16, q.device, stream)
     if max_len is None:
@@ -564,16 +597,19 @@ def paged_attention(q, cache, scale_kv, block_table, seq_lens, cu_q=None, max_q:
     need = lib.w4a8_paged_attention_workspace_size(ctypes.byref(view), heads, max_q, max_len)
     if need and workspace is None:
         workspace = _empty(need, torch.uint8, q.device, stream, returned=False)
+    elif workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace: expected a contiguous CUDA tensor on device {dev}")
     _check(lib.w4a8_paged_attention(
         q.data_ptr(), ldq, heads, ctypes.byref(view), max_q, max_len,
         dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
-        _heads("out", out, tokens, heads, dim),
+        _heads("out", out, dev, tokens, heads, dim),
         workspace.data_ptr() if workspace is not None else None,
         workspace.numel() * workspace.element_size() if workspace is not None else 0,
         _stream_of(q, stream)), "w4a8_paged_attention")
     return out
 
 
+@_on_device
 def read_probe(buf, offset: int, nbytes: int, workgroups: int, sink, stream=None):
     """Measurement aid: a read-only stream over nbytes of the uint8 CUDA tensor
     `buf` from byte `offset` (w4a8_read_probe); sink is an int32 CUDA tensor of
