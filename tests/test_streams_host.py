@@ -79,6 +79,7 @@ def seen(monkeypatch):
         monkeypatch.setattr(w4, "lib", Lib())
         monkeypatch.setattr(torch, "empty", recorded_empty)
         monkeypatch.setattr(torch.cuda, "stream", enter)
+        monkeypatch.setattr(torch.cuda, "set_stream", lambda stream: current.__setitem__(-1, stream))
         monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[-1])
         monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: current[-1].cuda_stream)
