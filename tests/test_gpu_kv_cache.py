@@ -412,6 +412,30 @@ def test_nothing_leaks_from_masked_pages(bad):
     assert np.isnan(o[112:128]).all()
 
 
+@pytest.mark.parametrize("bad", [np.inf, np.nan])
+@pytest.mark.parametrize("spans,heads,kv_heads,dim,cu", [
+    ([(90, 1), (90, 1), (2000, 1)], 8, 2, 128, False), ([(90, 1), (90, 9), (90, 70)], 16, 1, 128, True),
+    ([(90, 1), (90, 9), (90, 70)], 8, 2, 64, True), ([(90, 1), (90, 9), (90, 70)], 20, 1, 256, True),
+    ([(90, 90), (300, 300), (280, 257), (70, 70), (90, 40)], 128, 64, 128, True)])
+def test_a_key_scale_that_is_not_finite_is_seen(spans, heads, kv_heads, dim, cu, bad):
+    """Keys of a block whose scale is infinite or NaN make the rows that see
+    them NaN whatever the sign of their codes' product with the query, and
+    leave other sequences and other heads as they are."""
+    dev = device()
+    log(f"key scale {bad} heads={heads}/{kv_heads} dim={dim}")
+    batch = Batch(spans, 16, kv_heads, dim, 24, cu=cu)
+    q = batch.rng.standard_normal((batch.tokens, heads, dim)).astype(np.float16)
+    clean = attend(batch, q, dev)
+    batch.scale[batch.table[1, 2], 0, -1] = bad               # positions 32 .. 47, keys of the last kv head
+    o = attend(batch, q, dev)
+    hit = np.zeros(o.shape[:2], bool)
+    length, new = spans[1]
+    pos = np.arange(length - new, length)
+    hit[batch.cu[1]:batch.cu[2], -(heads // kv_heads):] = (pos >= 32)[:, None]
+    assert hit.any() and np.isnan(o[hit]).all()
+    assert np.array_equal(o[~hit].view(np.uint16), clean[~hit].view(np.uint16))
+
+
 def test_scores_far_apart_and_scales_far_apart():
     """One key holds all the weight, pages whose value scales differ by 2^20,
     pages of zeros, and a score scale of 0 (a plain mean)."""

@@ -14,6 +14,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "quant_common.h"
+
 namespace w4a8 {
 namespace attn {
 
@@ -29,6 +31,13 @@ static constexpr float kNone = -1.0e30f;
 static constexpr float kLift = 10.0f;
 // Scores more than 2^kRoom above a row's maximum move it (fp16 ends at 2^16).
 static constexpr float kRoom = 15.0f;
+
+// A page's key scale.  An infinite one becomes NaN, and with it the scores of its
+// keys: infinity times a negative sum would be the score of a masked key.
+static __device__ __forceinline__ float key_scale(uint32_t bits) {
+  const float s = dev::h2f(uint16_t(bits));
+  return s + (s - s);
+}
 
 // codes as unsigned bytes (code + 128), four at a time
 static __device__ __forceinline__ uint32_t biased(uint32_t w) { return w ^ 0x80808080u; }

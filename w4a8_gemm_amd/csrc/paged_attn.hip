@@ -200,7 +200,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void attn_split_kernel
     float x[8], rv[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const float sk = h2f(uint16_t(in.sk[u])) * p.scale_log2e * kCodeScale;
+      const float sk = key_scale(in.sk[u]) * p.scale_log2e * kCodeScale;
       // an all-zero page has scale 0: any positive value does, and the
       // smallest leaves the running maximum to the other pages
       const float sv = h2f(uint16_t(in.sv[u]));

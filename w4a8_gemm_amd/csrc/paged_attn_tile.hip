@@ -290,7 +290,7 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
       if (gthere) {
         const float sv = h2f(uint16_t(gsv));
         const float sv1 = sv == 0.0f ? 0x1p-24f : sv;   // as in paged_attn.hip
-        g.sk = h2f(uint16_t(gsk)) * factor;
+        g.sk = key_scale(gsk) * factor;
         g.lv = __builtin_amdgcn_logf(sv1);
         g.rv = __builtin_amdgcn_rcpf(sv1);
       }
