@@ -369,8 +369,9 @@ w4a8_status w4a8_silu_mul_quant(const uint16_t* gate_dev, int ldg,
  *   data   [num_pages][2][kv_heads][page_size][head_dim] int8 (0: keys,
  *          1: values), pages page_stride bytes apart
  *   scale  [num_pages][2][kv_heads] fp16, pages scale_stride values apart
- * A value is code * scale.  Strides larger than a page let the layers of a
- * model share one allocation.  The pool needs no initialisation.
+ * A value is code * scale; scales are not negative (a negative one gives
+ * unspecified results).  Strides larger than a page let the layers of a model
+ * share one allocation.  The pool needs no initialisation.
  *
  * A batch of sequences with new tokens is described by
  *   block_table  [batch][block_table_ld] int32: entry (b, i) is the page that

@@ -436,6 +436,24 @@ def test_a_key_scale_that_is_not_finite_is_seen(spans, heads, kv_heads, dim, cu,
     assert np.array_equal(o[~hit].view(np.uint16), clean[~hit].view(np.uint16))
 
 
+@pytest.mark.parametrize("spans,heads,kv_heads,dim,cu", [
+    ([(90, 1), (17, 1), (3000, 1)], 8, 2, 128, False), ([(90, 1), (90, 9), (90, 70)], 20, 1, 128, True)])
+def test_value_scale_zero_means_values_of_zero(spans, heads, kv_heads, dim, cu):
+    """A value is code * scale: codes under a value scale of 0 (a pool that was
+    not filled by rope_append) add nothing, and count in the softmax's sum."""
+    dev = device()
+    log(f"value scale 0 heads={heads}/{kv_heads} dim={dim}")
+    batch = Batch(spans, 16, kv_heads, dim, 25, cu=cu)
+    q = batch.rng.standard_normal((batch.tokens, heads, dim)).astype(np.float16)
+    batch.scale[:, 1] = 0
+    o = attend(batch, q, dev)
+    assert (o == 0).all()
+    # beside pages whose values are tiny as well
+    batch.scale[::2, 1] = 2.0 ** -24
+    batch.scale[1::4, 1] = np.float16(-0.0)
+    check_attention(batch, q, attend(batch, q, dev))
+
+
 def test_scores_far_apart_and_scales_far_apart():
     """One key holds all the weight, pages whose value scales differ by 2^20,
     pages of zeros, and a score scale of 0 (a plain mean)."""

@@ -198,13 +198,15 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void attn_split_kernel
     const int key0 = st * kStep;
     // scores, with the scales of their page
     float x[8], rv[2];
+    bool zero[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const float sk = key_scale(in.sk[u]) * p.scale_log2e * kCodeScale;
-      // an all-zero page has scale 0: any positive value does, and the
-      // smallest leaves the running maximum to the other pages
+      // an all-zero page has scale 0: for its weights any positive value does,
+      // and the smallest leaves the running maximum to the other pages
       const float sv = h2f(uint16_t(in.sv[u]));
-      const float sv1 = sv == 0.0f ? 0x1p-24f : sv;
+      zero[u] = sv == 0.0f;
+      const float sv1 = zero[u] ? 0x1p-24f : sv;
       const float lv = __builtin_amdgcn_logf(sv1);
       rv[u] = __builtin_amdgcn_rcpf(sv1);
       f32x4 acc = {0, 0, 0, 0};
@@ -237,7 +239,8 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void attn_split_kernel
     for (int i = 0; i < 8; ++i) {
       const float e = __builtin_amdgcn_exp2f(x[i] - m);
       sum[i >> 2] += e;
-      pt[i] = static_cast<_Float16>(e);
+      // whatever the codes of a page with scale 0 are, its values are 0
+      pt[i] = static_cast<_Float16>(zero[i >> 2] ? 0.0f : e);
     }
     // a sum of 0 (nothing seen) stays 0 whatever the page's scale holds
 #pragma unroll

@@ -79,7 +79,8 @@ __device__ __forceinline__ int v_place(int d, int c) {
 }
 
 struct GroupScale {   // of 16 keys
-  float sk, lv, rv, pad;
+  float sk, lv, rv;
+  float zero;         // 1: the value scale is 0, else 0
 };
 
 // Barrier of the workgroup that makes LDS writes visible and, unlike
@@ -290,6 +291,7 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
       if (gthere) {
         const float sv = h2f(uint16_t(gsv));
         const float sv1 = sv == 0.0f ? 0x1p-24f : sv;   // as in paged_attn.hip
+        g.zero = sv == 0.0f ? 1.0f : 0.0f;
         g.sk = key_scale(gsk) * factor;
         g.lv = __builtin_amdgcn_logf(sv1);
         g.rv = __builtin_amdgcn_rcpf(sv1);
@@ -388,6 +390,9 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
         g[n].rv = key < see_hi && key + 16 > see_lo ? g[n].rv : 0.0f;
       }
     }
+    float zeros = g[0].zero;
+#pragma unroll
+    for (int n = 1; n < kGroups; ++n) zeros += g[n].zero;
     float sum[kGroups];
     auto weights = [&]() {
 #pragma unroll
@@ -427,6 +432,13 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
     }
 #pragma unroll
     for (int n = 0; n < kGroups; ++n) l = __builtin_fmaf(sum[n], g[n].rv, l);
+    // whatever the codes of a page with scale 0 are, its values are 0
+    if (__builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, zeros)) != 0) {
+#pragma unroll
+      for (int n = 0; n < kGroups; ++n)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pt[n][i] = g[n].zero != 0.0f ? (_Float16)0.0f : pt[n][i];
+    }
   };
 
   // Each tile is a stretch of vector work (softmax of its scores) and one of
