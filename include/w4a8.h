@@ -449,7 +449,8 @@ w4a8_status w4a8_rope_append(const uint16_t* q_dev, int ldq, const uint16_t* k_d
  *   o = sum_t softmax_t(scale * q . k_t) v_t
  * over the positions t <= pos of the sequence (its query's own position),
  * and t > pos - window where window > 0.  Query head h reads kv head
- * h / (q_heads / kv_heads).  A row that sees no key is 0.
+ * h / (q_heads / kv_heads).  A row that sees no key is 0; one that sees a key
+ * and whose query holds a NaN or an infinity is NaN.
  *   q_dev, out_dev  rows of q_heads * head_dim fp16, 16-byte aligned, strides
  *                   a multiple of 8
  *   max_q, max_len  the most new tokens of one sequence and the longest

@@ -388,6 +388,27 @@ def test_absent_pages_are_not_seen():
     check_attention(batch, q, attend(batch, q, dev))
 
 
+@pytest.mark.parametrize("spans,heads,kv_heads,dim,cu", [
+    ([(1, 1), (2, 1), (40, 1)], 8, 2, 128, False), ([(3, 3), (200, 70), (30, 30)], 6, 2, 64, True),
+    ([(3, 3), (200, 70), (30, 30)], 6, 2, 128, True), ([(3, 3), (200, 70), (30, 30)], 6, 2, 256, True)])
+def test_queries_that_are_not_finite(spans, heads, kv_heads, dim, cu):
+    """A query head that holds a NaN or an infinity is NaN for every row, also
+    where all the scores that it sees are minus infinity; its neighbours stay
+    within their bound (their roundings may move: the 32 or 16 rows of a wave move
+    their running maxima together)."""
+    dev = device()
+    log(f"queries that are not finite heads={heads}/{kv_heads} dim={dim}")
+    batch = Batch(spans, 16, kv_heads, dim, 27, cu=cu)
+    q = batch.rng.standard_normal((batch.tokens, heads, dim)).astype(np.float16)
+    want, bound = dref.attention(q, batch.cache, batch.scale, batch.table, batch.lens, batch.cu, dim ** -0.5)
+    good = np.ones(heads, bool)
+    good[[1, 2, 4]] = False
+    q[:, 1, 7], q[:, 2, 5], q[:, 4, 0] = np.nan, np.inf, -np.inf
+    o = attend(batch, q, dev)
+    assert np.isnan(o[:, ~good]).all()
+    assert (np.abs(o.astype(np.float64) - want)[:, good] <= bound[:, good]).all()
+
+
 @pytest.mark.parametrize("bad", [np.nan, np.inf])
 def test_nothing_leaks_from_masked_pages(bad):
     """Scales that are NaN or infinite in pages a row does not see (later

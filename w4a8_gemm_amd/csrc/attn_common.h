@@ -39,6 +39,10 @@ static __device__ __forceinline__ float key_scale(uint32_t bits) {
   return s + (s - s);
 }
 
+// Queries as they enter the product: an infinity becomes NaN, and with it every
+// score of the row, where minus infinity would be the score of a masked key.
+static __device__ __forceinline__ half8_t query8(half8_t q) { return q + (q - q); }
+
 // codes as unsigned bytes (code + 128), four at a time
 static __device__ __forceinline__ uint32_t biased(uint32_t w) { return w ^ 0x80808080u; }
 

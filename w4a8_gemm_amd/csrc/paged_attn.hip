@@ -276,6 +276,10 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void attn_split_kernel
     while (st < last) {
       fetch(st, page, now);
       fetch_pages(st + kWaves, page);
+      if (st == first + wave) {       // here, so that the first keys are asked for before
+#pragma unroll
+        for (int i = 0; i < kKStep; ++i) q[i] = query8(q[i]);
+      }
       use(st, now);
       st += kWaves;
     }

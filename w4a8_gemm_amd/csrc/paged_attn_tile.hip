@@ -179,7 +179,7 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
         u = *reinterpret_cast<const uint4*>(src + d);
         u.x ^= flip, u.y ^= flip, u.z ^= flip, u.w ^= flip;
       }
-      q[i] = __builtin_bit_cast(half8_t, u);
+      q[i] = query8(__builtin_bit_cast(half8_t, u));
     }
   }
   const float factor = fabsf(p.scale_log2e) * kCodeScale;
