@@ -409,6 +409,27 @@ def test_queries_that_are_not_finite(spans, heads, kv_heads, dim, cu):
     assert (np.abs(o.astype(np.float64) - want)[:, good] <= bound[:, good]).all()
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_queries_that_are_not_finite_over_absent_pages(dim):
+    """A row that sees no key is 0 whatever its query holds; one that sees a
+    key is NaN."""
+    dev = device()
+    log(f"queries that are not finite over absent pages dim={dim}")
+    batch = Batch([(200, 40), (200, 40), (90, 1), (90, 1)], 16, 2, dim, 26)
+    batch.table[0] = -1
+    batch.table[2] = -1
+    batch.table[1, :12] = -1                       # positions below 192: its last 8 rows see the rest
+    q = batch.rng.standard_normal((82, 4, dim)).astype(np.float16)
+    q[:, 1], q[:, 2, 5] = np.nan, np.inf
+    o = attend(batch, q, dev)
+    assert (o[:72] == 0).all() and (o[80] == 0).all()
+    assert np.isnan(o[72:80, 1:3]).all() and np.isnan(o[81, 1:3]).all()
+    good = q.copy()
+    good[:, 1:3] = 0
+    want, bound = dref.attention(good, batch.cache, batch.scale, batch.table, batch.lens, batch.cu, dim ** -0.5)
+    assert (np.abs(o - want)[:, ::3] <= bound[:, ::3]).all()
+
+
 @pytest.mark.parametrize("bad", [np.nan, np.inf])
 def test_nothing_leaks_from_masked_pages(bad):
     """Scales that are NaN or infinite in pages a row does not see (later

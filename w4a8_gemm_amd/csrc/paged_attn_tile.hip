@@ -532,6 +532,21 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
   if (kTwoHalves && !behind) lds_barrier();
   l = pair_sum(l);
   if (!row_ok) return;
+  if (l != l) {
+    // keys of absent pages have weights exp2(-inf) = 0, but under a query that
+    // is not finite NaN: a row that sees no others is nothing all the same
+    const int hi = min(see_hi, range.hi);
+    bool any = false;
+    for (int key = max(see_lo, range.lo) & ~slot_mask; key < hi; key += slot_mask + 1)
+      any |= exists(table[key >> kv.page_shift]);
+    if (!any) {
+      l = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kDTiles; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
+    }
+  }
 
   // o[j][i] is column 32 j + 8 (i / 4) + 4 h + i % 4 of the lane's row
   if (p.splits == 1) {
