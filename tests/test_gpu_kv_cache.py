@@ -496,6 +496,30 @@ def test_value_scale_zero_means_values_of_zero(spans, heads, kv_heads, dim, cu):
     check_attention(batch, q, attend(batch, q, dev))
 
 
+@pytest.mark.parametrize("size", [3e8, -3e8, 1e20])
+@pytest.mark.parametrize("spans,heads,kv_heads,dim,cu", [
+    ([(40, 1), (2000, 1)], 8, 2, 128, False), ([(40, 9), (100, 30)], 8, 1, 128, True), ([(40, 9), (100, 30)], 8, 1, 64, True)])
+def test_scores_of_any_finite_size(spans, heads, kv_heads, dim, cu, size):
+    """Scores of +-1e8 to +-1e20, whose fp32 spacing is 8 or more: the largest one's key alone is left.  Its
+    value passes a reciprocal and three products in fp32."""
+    dev = device()
+    log(f"scores of {size} heads={heads}/{kv_heads} dim={dim}")
+    batch = Batch(spans, 16, kv_heads, dim, 28, cu=cu)
+    batch.scale[:, 0] = 0.01
+    for others, largest in ((-50, -40), (50, 60)):
+        batch.cache[:, 0] = others if size > 0 else -others
+        for b in range(len(spans)):                # at position 3, where every row sees it
+            batch.cache[batch.table[b, 0], 0, :, 3] = largest if size > 0 else -largest
+        q = np.full((batch.tokens, heads, dim), 1.0, np.float16)
+        o = attend(batch, q, dev, scale=size / dim).astype(np.float64)
+        for b in range(len(spans)):
+            at = batch.table[b, 0]
+            v = batch.cache[at, 1, :, 3].astype(np.float64) * batch.scale[at, 1].astype(np.float64)[:, None]
+            v = np.repeat(v, heads // kv_heads, axis=0)
+            rows = o[batch.cu[b]:batch.cu[b + 1]]
+            assert (np.abs(rows - v) <= dref.half_ulp16(v) * 1.001 + np.abs(v) * 2.0 ** -20).all()
+
+
 def test_scores_far_apart_and_scales_far_apart():
     """One key holds all the weight, pages whose value scales differ by 2^20,
     pages of zeros, and a score scale of 0 (a plain mean)."""

@@ -43,6 +43,13 @@ static __device__ __forceinline__ float key_scale(uint32_t bits) {
 // score of the row, where minus infinity would be the score of a masked key.
 static __device__ __forceinline__ half8_t query8(half8_t q) { return q + (q - q); }
 
+// A row's maximum, less the lift.  Scores from 2^27 on are 16 and more apart: the
+// difference may round to one that leaves fp16's range, and goes without then.
+static __device__ __forceinline__ float lifted(float mx) {
+  const float m = mx - kLift;
+  return mx - m > kRoom ? mx : m;
+}
+
 // codes as unsigned bytes (code + 128), four at a time
 static __device__ __forceinline__ uint32_t biased(uint32_t w) { return w ^ 0x80808080u; }
 

@@ -225,8 +225,8 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void attn_split_kernel
 #pragma unroll
     for (int i = 1; i < 8; ++i) mx = fmaxf(mx, x[i]);
     // a row moves its maximum only when a weight would leave fp16's range
-    if (__ballot(mx > m + kRoom)) {
-      const float m_new = fmaxf(m, row_max(mx) - kLift);
+    if (__ballot(mx - m > kRoom)) {
+      const float m_new = fmaxf(m, lifted(row_max(mx)));
       const float alpha = __builtin_amdgcn_exp2f(m - m_new);
       m = m_new;
       l *= alpha;

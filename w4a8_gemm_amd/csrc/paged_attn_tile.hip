@@ -394,14 +394,19 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
 #pragma unroll
     for (int n = 1; n < kGroups; ++n) zeros += g[n].zero;
     float sum[kGroups];
-    auto weights = [&]() {
+    auto weights = [&](auto again) {
 #pragma unroll
       for (int n = 0; n < kGroups; ++n) {
         const float c = g[n].lv - m;
         sum[n] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[n >> 1][8 * (n & 1) + i], g[n].sk, c));
+          // again: as the maximum was found, from the rounded score (a score of
+          // 2^27 and its rounding are up to 8 apart)
+          const float a = acc[n >> 1][8 * (n & 1) + i];
+          const float x = decltype(again)::value ? __builtin_fmaf(a, g[n].sk, g[n].lv) - m
+                                                 : __builtin_fmaf(a, g[n].sk, c);
+          const float e = __builtin_amdgcn_exp2f(x);
           // summed before the rounding: a weight carries its page's value
           // scale, and where that is far below the others' the rounded weight
           // has few bits or none, while its part of the sum, once the scale is
@@ -411,7 +416,7 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
         }
       }
     };
-    weights();
+    weights(std::false_type());
     float most = sum[0];
 #pragma unroll
     for (int n = 1; n < kGroups; ++n) most += sum[n];
@@ -422,13 +427,13 @@ __global__ __launch_bounds__(64 * NW, DP == 256 ? 1 : 2) void attn_tile_kernel(A
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           mx = fmaxf(mx, __builtin_fmaf(acc[n >> 1][8 * (n & 1) + i], g[n].sk, g[n].lv));
-      const float m_new = fmaxf(m, pair_max(mx) - kLift);
+      const float m_new = fmaxf(m, lifted(pair_max(mx)));
       const float alpha = __builtin_amdgcn_exp2f(m - m_new);
       m = m_new;
       l *= alpha;
 #pragma unroll
       for (int i = 0; i < kDTiles; ++i) o[i] *= alpha;
-      weights();
+      weights(std::true_type());
     }
 #pragma unroll
     for (int n = 0; n < kGroups; ++n) l = __builtin_fmaf(sum[n], g[n].rv, l);
