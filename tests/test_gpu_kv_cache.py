@@ -496,11 +496,11 @@ def test_value_scale_zero_means_values_of_zero(spans, heads, kv_heads, dim, cu):
     check_attention(batch, q, attend(batch, q, dev))
 
 
-@pytest.mark.parametrize("size", [3e8, -3e8, 1e20])
+@pytest.mark.parametrize("size", [3e8, -3e8, 1e20, -1e32, 1e34])
 @pytest.mark.parametrize("spans,heads,kv_heads,dim,cu", [
     ([(40, 1), (2000, 1)], 8, 2, 128, False), ([(40, 9), (100, 30)], 8, 1, 128, True), ([(40, 9), (100, 30)], 8, 1, 64, True)])
 def test_scores_of_any_finite_size(spans, heads, kv_heads, dim, cu, size):
-    """Scores of +-1e8 to +-1e20, whose fp32 spacing is 8 or more: the largest one's key alone is left.  Its
+    """Scores of +-1e8 to +-1e34, whose fp32 spacing is 8 or more: the largest one's key alone is left.  Its
     value passes a reciprocal and three products in fp32."""
     dev = device()
     log(f"scores of {size} heads={heads}/{kv_heads} dim={dim}")

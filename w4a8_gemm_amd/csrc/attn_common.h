@@ -23,8 +23,8 @@ typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// A finite "no key yet": exp2(-inf - kNone) is 0, not NaN.
-static constexpr float kNone = -1.0e30f;
+// A finite "no key yet", below every score: exp2(-inf - kNone) is 0, not NaN.
+static constexpr float kNone = -3.4028235e38f;
 // Softmax weights are kept up to 2^kLift, so that weights down to 2^-(24 +
 // kLift) of the largest still register in fp16; the sum carries the same
 // factor and the quotient drops it.
