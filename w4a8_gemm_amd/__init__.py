@@ -401,9 +401,21 @@ def _int8_out(m, k, a8, s_a, like, stream):
     return a8, s_a
 
 
+INT_MAX = 2 ** 31 - 1
+
+
+def _int(name, v):
+    """v as the C interface's int: ctypes would pass its low 32 bits."""
+    if not 0 <= v <= INT_MAX:
+        raise ValueError(f"{name}: {v} is not in 0 .. {INT_MAX}")
+    return v
+
+
 def _ld(t):
     """Row stride of a 2-D tensor (a single row's stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    m, k = t.shape
+    ld = t.stride(0) if m > 1 else max(t.stride(0), k)
+    return ld if ld <= INT_MAX and m <= INT_MAX else _int("rows or row stride", max(ld, m))
 
 
 @_on_device
@@ -523,13 +535,14 @@ def _kv_view(cache, scale, block_table, seq_lens, cu_q, q):
         _vector("cu_q", cu_q, torch.int32, dev, batch + 1)
     elif total_q != batch:
         raise ValueError(f"without cu_q each of the {batch} sequences brings one token, got {total_q}")
+    table_ld = block_table.stride(0) if batch > 1 else max(block_table.stride(0), max_pages)
+    if table_ld > INT_MAX or batch > INT_MAX or pages > INT_MAX:
+        _int("pages, sequences or the block table's row stride", max(table_ld, batch, pages))
     return KvView(cache.data_ptr(), scale.data_ptr(),
                   cache.stride(0) if pages > 1 else 2 * heads * page * dim,
                   scale.stride(0) if pages > 1 else 2 * heads, pages, page, heads, dim,
-                  block_table.data_ptr(),
-                  block_table.stride(0) if batch > 1 else max(block_table.stride(0), max_pages),
-                  max_pages, seq_lens.data_ptr(), cu_q.data_ptr() if cu_q is not None else None,
-                  batch, total_q)
+                  block_table.data_ptr(), table_ld, max_pages, seq_lens.data_ptr(),
+                  cu_q.data_ptr() if cu_q is not None else None, batch, total_q)
 
 
 def _heads(name, t, dev, tokens=None, heads=None, dim=None):
@@ -546,7 +559,8 @@ def _heads(name, t, dev, tokens=None, heads=None, dim=None):
     s = t.stride()
     if s[2] != 1 or (h > 1 and s[1] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s[0] if n > 1 else max(s[0], h * d)
+    ld = s[0] if n > 1 else max(s[0], h * d)
+    return ld if ld <= INT_MAX and n <= INT_MAX else _int(f"{name}: tokens or row stride", max(ld, n))
 
 
 @_on_device
@@ -569,6 +583,7 @@ def rope_append(q, k, v, cos_sin, cache, scale, block_table, seq_lens, cu_q=None
         if cos_sin.get_device() != dev:
             raise _elsewhere("cos_sin", cos_sin, dev)
         max_pos, rotary = cos_sin.shape
+        _int("cos_sin: positions or rotary_dim", max(max_pos, rotary))
     if out is None:
         out = _empty((tokens, heads, dim), torch.float16, q.device, stream)
     _check(lib.w4a8_rope_append(
@@ -597,6 +612,8 @@ def paged_attention(q, cache, scale_kv, block_table, seq_lens, cu_q=None, max_q:
         max_len = view.max_pages * view.page_size
     if max_q is None:
         max_q = 1 if cu_q is None else tokens
+    # a bound or a window beyond any sequence is none
+    max_q, max_len, window = min(max_q, INT_MAX), min(max_len, INT_MAX), min(window, INT_MAX)
     need = lib.w4a8_paged_attention_workspace_size(ctypes.byref(view), heads, max_q, max_len)
     if need and workspace is None:
         workspace = _empty(need, torch.uint8, q.device, stream, returned=False)
