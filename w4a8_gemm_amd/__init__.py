@@ -198,13 +198,12 @@ def _on_device(fn):
         index = (args[0] if args else kw[params[0]]).get_device()
         if index < 0:
             return fn(*args, **kw)          # fn refuses it
-        cuda = torch.cuda
         stream = args[at] if len(args) > at else kw.get("stream")
         if stream is not None and stream.device.index != index:
             raise ValueError(f"stream: expected one of cuda:{index}, got one of {stream.device}")
-        if index == cuda.current_device():
+        if index == torch.cuda.current_device():
             return fn(*args, **kw)
-        with cuda.device(index):
+        with torch.cuda.device(index):
             return fn(*args, **kw)
     return call
 
@@ -585,12 +584,13 @@ def rope_append(q, k, v, cos_sin, cache, scale, block_table, seq_lens, cu_q=None
         max_pos, rotary = cos_sin.shape
         _int("cos_sin: positions or rotary_dim", max(max_pos, rotary))
     if out is None:
-        out = _empty((tokens, heads, dim), torch.float16, q.device, stream)
+        out, ldo = _empty((tokens, heads, dim), torch.float16, q.device, stream), heads * dim
+    else:
+        ldo = _heads("out", out, dev, tokens, heads, dim)
     _check(lib.w4a8_rope_append(
         q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, heads,
         cos_sin.data_ptr() if cos_sin is not None else None, rotary, max_pos, int(interleaved),
-        ctypes.byref(view), out.data_ptr(), _heads("out", out, dev, tokens, heads, dim),
-        _stream_of(q, stream)), "w4a8_rope_append")
+        ctypes.byref(view), out.data_ptr(), ldo, _stream_of(q, stream)), "w4a8_rope_append")
     return out
 
 
@@ -607,13 +607,16 @@ def paged_attention(q, cache, scale_kv, block_table, seq_lens, cu_q=None, max_q:
     view = _kv_view(cache, scale_kv, block_table, seq_lens, cu_q, q)
     ldq = _heads("q", q, dev, tokens, None, view.head_dim)
     if out is None:
-        out = _empty((tokens, heads, dim), torch.float16, q.device, stream)
+        out, ldo = _empty((tokens, heads, dim), torch.float16, q.device, stream), heads * dim
+    else:
+        ldo = _heads("out", out, dev, tokens, heads, dim)
     if max_len is None:
         max_len = view.max_pages * view.page_size
     if max_q is None:
         max_q = 1 if cu_q is None else tokens
     # a bound or a window beyond any sequence is none
-    max_q, max_len, window = min(max_q, INT_MAX), min(max_len, INT_MAX), min(window, INT_MAX)
+    if max_q > INT_MAX or max_len > INT_MAX or window > INT_MAX:
+        max_q, max_len, window = min(max_q, INT_MAX), min(max_len, INT_MAX), min(window, INT_MAX)
     need = lib.w4a8_paged_attention_workspace_size(ctypes.byref(view), heads, max_q, max_len)
     if need and workspace is None:
         workspace = _empty(need, torch.uint8, q.device, stream, returned=False)
@@ -621,8 +624,7 @@ def paged_attention(q, cache, scale_kv, block_table, seq_lens, cu_q=None, max_q:
         raise ValueError(f"workspace: expected a contiguous CUDA tensor on device {dev}")
     _check(lib.w4a8_paged_attention(
         q.data_ptr(), ldq, heads, ctypes.byref(view), max_q, max_len,
-        dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
-        _heads("out", out, dev, tokens, heads, dim),
+        dim ** -0.5 if scale is None else scale, window, out.data_ptr(), ldo,
         workspace.data_ptr() if workspace is not None else None,
         workspace.numel() * workspace.element_size() if workspace is not None else 0,
         _stream_of(q, stream)), "w4a8_paged_attention")
