@@ -51,6 +51,40 @@ def test_norm(m, k, residual):
     dref.check_int8_rows(a8, s_a, y)
 
 
+# every threads-and-chunks form of rows held in registers: for norm of few rows
+# (one chunk a thread, then 1024 threads), of many (up to 4 chunks), the last
+# chunk whole or not
+FEW = [(3, 2048), (3, 4096), (2, 4104), (2, 8192), (2, 8200), (2, 16392), (1, 24584), (2, 32768)]
+MANY = [(512, 2048), (513, 2056), (512, 4096), (600, 5128), (600, 8192), (512, 8200), (530, 12296),
+        (512, 16384), (512, 16392), (515, 24584), (512, 32768)]
+
+
+@pytest.mark.parametrize("residual", [True, False])
+@pytest.mark.parametrize("m,k", FEW + MANY)
+def test_norm_held_forms(m, k, residual):
+    import torch
+    dev = device()
+    log(f"norm held m={m} k={k} residual={residual}")
+    x, r = rows(m, k, 15), rows(m, k, 16, 3.0) if residual else None
+    w = (1 + 0.3 * np.random.default_rng(17).standard_normal(k)).astype(np.float16)
+    h, a8, s_a = norm(torch.from_numpy(x).to(dev), torch.from_numpy(w).to(dev),
+                      torch.from_numpy(r).to(dev) if residual else None)
+    want_h, y = dref.rms_norm(x, r, w, EPS)
+    assert np.array_equal(h.view(np.uint16), want_h.view(np.uint16))
+    dref.check_int8_rows(a8, s_a, y)
+
+
+@pytest.mark.parametrize("m,k", FEW + [(513, 2048), (512, 4104), (600, 8192)])
+def test_silu_mul_held_forms(m, k):
+    import torch
+    dev = device()
+    log(f"silu_mul held m={m} k={k}")
+    g, u = rows(m, k, 18, 2.0), rows(m, k, 19)
+    a8, s_a = w4.silu_mul_quant(torch.from_numpy(g).to(dev), torch.from_numpy(u).to(dev))
+    torch.cuda.synchronize()
+    dref.check_int8_rows(a8.cpu().numpy(), s_a.cpu().numpy(), dref.silu_mul(g, u), dref.FP32 + 64 * 2.0 ** -23)
+
+
 @pytest.mark.parametrize("pad,into", [(8, "new"), (3, "new"), (0, "x"), (16, "residual"), (0, "residual")])
 @pytest.mark.parametrize("m,k", [(6, 4096), (5, 300), (3, 33000)])
 def test_norm_strides_and_in_place(m, k, pad, into):
