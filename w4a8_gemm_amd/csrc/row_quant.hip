@@ -14,7 +14,6 @@
 // a launch's latency.
 
 #include <hip/hip_runtime.h>
-#include <limits.h>
 #include <stdint.h>
 
 #include "decoder_kernels.h"
@@ -341,15 +340,16 @@ __global__ __launch_bounds__(T) void silu_mul_quant_held_kernel(SwigluParams p) 
   }
 }
 
-// Threads and chunks of a held row.  With many rows a few waves a row are
-// enough and spend less on the reduction; with few, every thread takes one
-// chunk if the row allows it, so that the loads of a row are all out at once.
+// Threads and chunks of a held row, with up to `most` chunks a thread before
+// the threads are doubled (1024 threads take up to 4 in any case).  With many
+// rows a few waves a row are enough and spend less on the reduction; with few,
+// every thread takes one chunk if the row allows it, so that the loads of a
+// row are all out at once.
 struct Held {
   int threads, chunks;      // threads 0: the row is too long
 };
-Held held_plan(int m, int k, int many) {
+Held held_plan(int m, int k, int most) {
   const int n = (k + 7) / 8;
-  const int most = m >= many ? 4 : 1;
   int t = 256;
   while (t < 1024 && n > most * t) t *= 2;
   // a launch holds fewer than 2^32 threads
@@ -357,17 +357,29 @@ Held held_plan(int m, int k, int many) {
   return {t, (n + t - 1) / t};
 }
 
-#define W4A8_HELD(kernel, h)                                                        \
-  ((h).threads == 256   ? (h).chunks == 1   ? reinterpret_cast<const void*>(&kernel<256, 1>)  \
-                          : (h).chunks == 2 ? reinterpret_cast<const void*>(&kernel<256, 2>)  \
-                                            : reinterpret_cast<const void*>(&kernel<256, 4>)  \
-   : (h).threads == 512 ? (h).chunks == 1   ? reinterpret_cast<const void*>(&kernel<512, 1>)  \
-                          : (h).chunks <= 3 ? reinterpret_cast<const void*>(&kernel<512, 3>)  \
-                                            : reinterpret_cast<const void*>(&kernel<512, 4>)  \
-                        : (h).chunks == 1   ? reinterpret_cast<const void*>(&kernel<1024, 1>) \
-                          : (h).chunks == 2 ? reinterpret_cast<const void*>(&kernel<1024, 2>) \
-                          : (h).chunks == 3 ? reinterpret_cast<const void*>(&kernel<1024, 3>) \
-                                            : reinterpret_cast<const void*>(&kernel<1024, 4>))
+const void* norm_held(const Held& h) {
+  if (h.threads == 256)
+    return h.chunks == 1   ? reinterpret_cast<const void*>(&rms_norm_quant_held_kernel<256, 1>)
+           : h.chunks == 2 ? reinterpret_cast<const void*>(&rms_norm_quant_held_kernel<256, 2>)
+                           : reinterpret_cast<const void*>(&rms_norm_quant_held_kernel<256, 4>);
+  if (h.threads == 512)
+    return h.chunks == 1   ? reinterpret_cast<const void*>(&rms_norm_quant_held_kernel<512, 1>)
+           : h.chunks <= 3 ? reinterpret_cast<const void*>(&rms_norm_quant_held_kernel<512, 3>)
+                           : reinterpret_cast<const void*>(&rms_norm_quant_held_kernel<512, 4>);
+  return h.chunks == 1   ? reinterpret_cast<const void*>(&rms_norm_quant_held_kernel<1024, 1>)
+         : h.chunks == 2 ? reinterpret_cast<const void*>(&rms_norm_quant_held_kernel<1024, 2>)
+         : h.chunks == 3 ? reinterpret_cast<const void*>(&rms_norm_quant_held_kernel<1024, 3>)
+                         : reinterpret_cast<const void*>(&rms_norm_quant_held_kernel<1024, 4>);
+}
+
+const void* silu_mul_held(const Held& h) {
+  if (h.threads == 256) return reinterpret_cast<const void*>(&silu_mul_quant_held_kernel<256, 1>);
+  if (h.threads == 512) return reinterpret_cast<const void*>(&silu_mul_quant_held_kernel<512, 1>);
+  return h.chunks == 1   ? reinterpret_cast<const void*>(&silu_mul_quant_held_kernel<1024, 1>)
+         : h.chunks == 2 ? reinterpret_cast<const void*>(&silu_mul_quant_held_kernel<1024, 2>)
+         : h.chunks == 3 ? reinterpret_cast<const void*>(&silu_mul_quant_held_kernel<1024, 3>)
+                         : reinterpret_cast<const void*>(&silu_mul_quant_held_kernel<1024, 4>);
+}
 
 bool rows16(const void* p, int ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
 bool rows8(const void* p, int ld) { return reinterpret_cast<uintptr_t>(p) % 8 == 0 && ld % 8 == 0; }
@@ -380,10 +392,9 @@ hipError_t launch_rms_norm_quant(const NormParams& p, hipStream_t stream) {
                    rows8(p.a8, p.lda8);
   NormParams q = p;
   void* args[] = {&q};
-  const Held held = held_plan(p.m, p.k, kManyRows);
+  const Held held = held_plan(p.m, p.k, p.m >= kManyRows ? 4 : 1);
   if (vec && held.threads)
-    return hipLaunchKernel(W4A8_HELD(rms_norm_quant_held_kernel, held), dim3(p.m),
-                           dim3(held.threads), args, 0, stream);
+    return hipLaunchKernel(norm_held(held), dim3(p.m), dim3(held.threads), args, 0, stream);
   const void* fn = vec ? reinterpret_cast<const void*>(&rms_norm_quant_kernel<true>)
                        : reinterpret_cast<const void*>(&rms_norm_quant_kernel<false>);
   return hipLaunchKernel(fn, dim3(p.m), dim3(kThreads), args, 0, stream);
@@ -394,10 +405,9 @@ hipError_t launch_silu_mul_quant(const SwigluParams& p, hipStream_t stream) {
                    rows8(p.a8, p.lda8);
   SwigluParams q = p;
   void* args[] = {&q};
-  const Held held = held_plan(p.m, p.k, INT_MAX);
+  const Held held = held_plan(p.m, p.k, 1);
   if (vec && held.threads)
-    return hipLaunchKernel(W4A8_HELD(silu_mul_quant_held_kernel, held), dim3(p.m),
-                           dim3(held.threads), args, 0, stream);
+    return hipLaunchKernel(silu_mul_held(held), dim3(p.m), dim3(held.threads), args, 0, stream);
   const void* fn = vec ? reinterpret_cast<const void*>(&silu_mul_quant_kernel<true>)
                        : reinterpret_cast<const void*>(&silu_mul_quant_kernel<false>);
   return hipLaunchKernel(fn, dim3(p.m), dim3(kThreads), args, 0, stream);
