@@ -481,10 +481,10 @@ def rope_table(max_pos: int, rotary_dim: int, base: float = 10000.0, scaling: st
              "base":   base * factor^(rotary_dim / (rotary_dim - 2)), which
                        leaves the highest frequency and divides the lowest by
                        factor
-             "bands":  frequencies that turn fewer than `low` times within
-                       original_max_pos / factor, those that turn more than
-                       `high` times kept, a linear blend between (the scheme
-                       of Llama-3.1's checkpoints)
+             "bands":  by the turns within original_max_pos: frequencies of
+                       fewer than `low` divided by factor, those of more than
+                       `high` kept, a linear blend between (the scheme of
+                       Llama-3.1's checkpoints)
     """
     if max_pos < 1 or rotary_dim < 2 or rotary_dim % 2:
         raise ValueError("rope_table: max_pos >= 1 and an even rotary_dim >= 2 are needed")

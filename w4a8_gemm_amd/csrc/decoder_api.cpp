@@ -92,12 +92,14 @@ AttnPlan plan_attn(const KvArgs& kv, int q_heads, int max_q, int max_len) {
   //   16-row tiles: 24 workgroups a compute unit even out ragged lengths
   //   (64 x up to 8192 keys: 6 a unit 142 us, 12 137, 24 131).
   //   Tiles of 128 or more rows: where the partial results, 4 bytes a value
-  //   each way, are few, 3 a unit (16 x 8 tokens over 4000 keys, 0.3 M values:
-  //   81 us with 2, 56 with 3; 3 x 700 over 1400 with heads of 64, 1.4 M: 52
-  //   and 44), unless the tiles make 2 a unit by themselves.  Where they are
-  //   many, 2, and only if the tiles make less than one (512 tokens over 8000
-  //   keys, 2.1 M: 126 us with 2, 136 with 3; 2000 tokens over themselves, 8 M:
-  //   71 us unsplit, 123 split).
+  //   each way, are few, 3 a unit, unless the tiles make 2 a unit by themselves;
+  //   where they are many, 2, and only if the tiles make less than one.  As many
+  //   and as few, us: 16 x 8 tokens over 4000 keys (0.3 M values) 81 and 56,
+  //   16 x 16 over 2048 (0.5 M) 59 and 40, 256 over 8000 (1.0 M) 83 and 72, 366
+  //   over 8000 (1.5 M) 119 and 109, 3 x 700 over 1400 with heads of 64 (1.5 M)
+  //   52 and 42; 440 over 8000 (1.8 M) 102 and 126, 512 over 8000 (2.1 M) 120 and
+  //   134, 2000 over themselves (8 M) 71 and 123.  16 x 64 over 2048 (2.7 M) would
+  //   gain from few, 77 and 73; most others between are equal.
   const long rows_all = long(kv.total_q) * q_heads;
   const bool few = rows_all * kv.dim <= kFewPartials;
   const long target = (!pl.waves ? 24 : few ? 3 : 2) * kComputeUnits;

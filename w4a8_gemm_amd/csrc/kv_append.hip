@@ -13,9 +13,11 @@
 // and j + rotary/2 in the half layout, 2j and 2j + 1 in the interleaved one),
 // or 16 values that are not rotated.
 //
-// Measured: the next token of 64 sequences (32 + 8 heads of 128) 4.7 us, a
-// launch's latency; 4 prompts of up to 1500 tokens (110 MB) 24.6 us = 4.5 TB/s,
-// where a large copy reaches 5.2.
+// Measured: the next token of 64 sequences (32 + 8 heads of 128) 4.7 us, the
+// latency of a launch and of loads that wait for each other (lengths, page number,
+// the page's scale); 4 prompts of up to 1500 tokens (110 MB) 30 us = 3.7 TB/s
+// into outputs that are not cached, 24.4 into the same ones, where a large copy
+// reaches 5.2 TB/s.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

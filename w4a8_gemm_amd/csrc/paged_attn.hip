@@ -20,10 +20,11 @@
 // neighbouring values of one row.
 //
 // Bound by memory: every key and value byte is read once.  Measured, graph
-// replays with the join: 64 sequences of up to 8192 keys (673 MB) 136 us =
-// 4.95 TB/s, 16 x 64 heads x up to 4000 keys in pages of 16 (637 MB) 127 us =
-// 5.0 TB/s, two of up to 131072 (366 MB) 83 us = 4.4 TB/s, where a large
-// copy reaches 5.2 TB/s; one of 2001 keys 9.3 us, latency.
+// replays with the join: 64 sequences of up to 8192 keys (673 MB) 132 to 136 us =
+// 5.0 TB/s, 16 x 64 heads x up to 4000 keys in pages of 16 (637 MB) 124 to 127 us
+// = 5.1 TB/s, two of up to 131072 (366 MB) 81 to 84 us = 4.4 TB/s, where a large
+// copy reaches 5.2 TB/s and a kernel that only reads 6 to 7; one of 2001 keys
+// 9.4 us, two launches and their chains of loads.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

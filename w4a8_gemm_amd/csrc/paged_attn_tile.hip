@@ -17,9 +17,12 @@
 // Bound by the matrix and vector instructions of a tile (per wave and 64 keys
 // 1024 cycles of products, about 700 of softmax and 250 of staging) and the
 // first LDS reads after each barrier, some 500 cycles under load.  Measured: a
-// prompt of 8192 tokens, 32 + 8 heads of 128, 600 us = 0.92 PFLOP/s of the
-// causal half (a library's fp16 matrix product 8192^3 reaches 1.15); 12 ragged
-// chunks of up to 200 tokens over a window of 1024 63 us, few workgroups.
+// prompt of 8192 tokens, 32 + 8 heads of 128, 580 to 610 us = 0.90 to 0.95
+// PFLOP/s of the causal half (a library's fp16 matrix product 8192^3 reaches
+// 1.15).  Where the tiles are few, the time is that of the longest chain of key
+// tiles in a workgroup, 2 us a tile with one workgroup on a unit: 12 ragged
+// chunks of up to 200 tokens over a window of 1024 64 us, a prompt of 2000 tokens
+// 71, 16 x up to 64 tokens over 2048 keys 76.
 // 128 rows a workgroup instead of 256 take 640 us on the prompt, but 67
 // against 98 us on the chunks, which 256 rows leave on too few units.
 

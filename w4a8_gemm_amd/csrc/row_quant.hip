@@ -8,10 +8,12 @@
 //   y = rstd * (h * w), and rounding rstd * t is monotone in |t|, so
 //   max|y| = rstd * max|h * w| exactly as the codes see it.
 //
-// Bound by memory: rows stay in registers, so every byte moves once.  Norm of
-// 4096 x 8192 with residual (235 MB) 41 us = 5.7 TB/s, SwiGLU of 2048 x 24576
-// (252 MB) 47 us = 5.4 TB/s; a large copy reaches 5.2.  8 rows of 4096: 3.7 us,
-// a launch's latency.
+// Bound by memory: rows stay in registers, so every byte moves once.  Over
+// buffers that are not in the last-level cache, norm of 4096 x 8192 with residual
+// (235 MB) takes 47 us = 5.0 TB/s, SwiGLU of 2048 x 24576 (252 MB) 51 us = 5.0
+// TB/s; a large copy reaches 5.1 to 5.2.  On the same outputs again and again,
+// partly cached, 41 and 47.  8 rows of 4096: 3.7 us, latency: the launch (1.5),
+// one load from memory, the reduction through LDS, the codes' store.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
