@@ -477,6 +477,210 @@ w4a8_status w4a8_paged_attention(const uint16_t* q_dev, int ldq, int q_heads,
                                  int window, uint16_t* out_dev, int ldo, void* workspace_dev,
                                  size_t workspace_bytes, void* stream);
 
+/* As w4a8_rope_append, with the positions of the angles given: positions_dev
+ * [total_q] int32, for drafted trees, whose tokens' places in the cache and in
+ * their sentence differ.  Positions outside [0, max_pos) take the nearest row.
+ * NULL: the places in the cache. */
+w4a8_status w4a8_rope_append_at(const uint16_t* q_dev, int ldq, const uint16_t* k_dev, int ldk,
+                                const uint16_t* v_dev, int ldv, int q_heads,
+                                const float* cos_sin_dev, int rotary_dim, int max_pos,
+                                int interleaved, const int32_t* positions_dev,
+                                const w4a8_kv_view* view, uint16_t* q_out_dev, int ldqo,
+                                void* stream);
+
+/* ------------------------------------------------------ drafted token trees
+ * Speculative decoding: a sequence's new tokens are a tree of drafted ones
+ * behind its certain ones, several continuations of one text at once.  Its nodes
+ * are numbered from 0 (the sequence's new token rows, in order), parents before
+ * children: parents_dev [total_q] int32 holds each node's parent within its
+ * sequence, anything outside [0, node) meaning none.  A step is
+ *   w4a8_tree_mask       who sees whom, and at which position
+ *   w4a8_rope_append_at, w4a8_tree_attention  in each layer
+ *   w4a8_sample          a token for every node
+ *   w4a8_tree_accept     which nodes the sampled tokens confirm
+ *   w4a8_kv_keep         in each layer: their keys and values moved together
+ * cu_q_dev, seq_lens_dev, batch and total_q are as in w4a8_kv_view; without
+ * cu_q_dev every sequence has one node. */
+
+/* The mask of w4a8_tree_attention and the positions of w4a8_rope_append_at:
+ * bit j % 32 of word mask[t][j / 32] says whether new token t sees its sequence's
+ * node j, which it does for itself and all above it; a node's position is that of
+ * the sequence's last certain token and its depth, seq_len - nodes + depth.
+ *   mask_dev       [total_q][mask_ld] uint32, mask_words of each row written;
+ *                  nodes from 32 * mask_words on have no bit
+ *   positions_dev  [total_q] int32, may be NULL
+ * batch or total_q of 0 is a no-op.  Errors: INVALID_ARGUMENT, DEVICE. */
+w4a8_status w4a8_tree_mask(const int32_t* parents_dev, const int32_t* seq_lens_dev,
+                           const int32_t* cu_q_dev, int batch, int total_q, uint32_t* mask_dev,
+                           int mask_ld, int mask_words, int32_t* positions_dev, void* stream);
+
+/* Attention of drafted tokens over the cache, which holds them already: as
+ * w4a8_paged_attention, but a row sees all positions before its sequence's new
+ * tokens, and of those the ones that its mask names (any mask, not only a
+ * tree's; it need not name the token itself).  With window > 0 only the last
+ * `window` of all that the row sees count: of a tree's path and the text before.
+ * A row that sees nothing is 0.
+ *   mask_dev   [total_q][mask_ld] uint32 as w4a8_tree_mask writes it; nodes from
+ *              32 * mask_words on are not seen
+ *   workspace  w4a8_tree_attention_workspace_size bytes, as there
+ * Errors as w4a8_paged_attention. */
+size_t w4a8_tree_attention_workspace_size(const w4a8_kv_view* view, int q_heads, int max_q,
+                                          int max_len);
+w4a8_status w4a8_tree_attention(const uint16_t* q_dev, int ldq, int q_heads,
+                                const w4a8_kv_view* view, const uint32_t* mask_dev, int mask_ld,
+                                int mask_words, int max_q, int max_len, float scale, int window,
+                                uint16_t* out_dev, int ldo, void* workspace_dev,
+                                size_t workspace_bytes, void* stream);
+
+/* The nodes that sampled tokens confirm.  Node 0, the sequence's last certain
+ * token, is confirmed; after a confirmed node the first of its children with
+ * drafted[child] == sampled[node] is, and so on.
+ *   drafted_dev   [total_q] int32, the token of each node
+ *   sampled_dev   [total_q] int32, the token drawn after each node; a negative one
+ *                 (nothing to draw) confirms no child
+ *   path_dev      [batch][path_ld] int32: the confirmed nodes in order, then -1
+ *                 up to max_path; no more than max_path are confirmed
+ *   count_dev     [batch] int32, their number
+ *   tokens_dev    [batch] int32, the token drawn after the last of them: the
+ *                 sequence's next one, -1 where there are no nodes
+ *   new_lens_dev  [batch] int32, seq_len - nodes + count (may be seq_lens_dev,
+ *                 if w4a8_kv_keep does not follow)
+ * batch of 0 is a no-op.  Errors: INVALID_ARGUMENT, DEVICE. */
+w4a8_status w4a8_tree_accept(const int32_t* drafted_dev, const int32_t* parents_dev,
+                             const int32_t* sampled_dev, const int32_t* seq_lens_dev,
+                             const int32_t* cu_q_dev, int batch, int total_q, int32_t* path_dev,
+                             int path_ld, int max_path, int32_t* count_dev, int32_t* tokens_dev,
+                             int32_t* new_lens_dev, void* stream);
+
+/* Keys and values of confirmed nodes moved to the places behind the sequence's
+ * certain tokens: node path[b][i] to place i, for i < count[b].  The view is that
+ * of the step before (seq_lens with all nodes).  Paths ascend; a node that is
+ * below its place or not in the sequence leaves the place as it is.
+ * A page that gets tokens has afterwards, with s the scales before,
+ *   s' = the largest s of the pages its tokens come from, and its own if it holds
+ *        earlier tokens of the sequence
+ *   codes moved from a page with s, and earlier ones: rint(code * fp32(s / s'))
+ * so within a page codes move as they are.  Slots of other tokens keep codes
+ * that mean nothing.  batch or total_q of 0 is a no-op.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (as w4a8_rope_append), DEVICE. */
+w4a8_status w4a8_kv_keep(const w4a8_kv_view* view, const int32_t* path_dev, int path_ld,
+                         int max_path, const int32_t* count_dev, void* stream);
+
+/* ---------------------------------------------------------------- sampling
+ * A token for each row of logits from a given random number.
+ *   w[i] = exp((x[i] - max x) / temperature)
+ * In the order of falling logits, equal ones in the order of their numbers, the
+ * first n tokens are kept, n the smallest of
+ *   top_k            (if > 0)
+ *   the fewest whose weights add up to top_p of those of the top_k (if < 1; one
+ *                    at least)
+ *   the number with w >= min_p (more than 1 counts as 1)
+ * The token is the first one, in the order of numbers, up to which the kept
+ * weights add up to more than u times their sum.  Weights are computed in 64 bits
+ * and held as multiples of 2^-44; a token with less is never drawn.
+ * temperature 0 takes the largest logit, the first of equals.
+ *   logits_dev   rows x vocab fp16, or fp32 where logits_f32 is not 0, row stride
+ *                ld elements, any alignment.  Minus infinity excludes a token.
+ *   u_dev        [rows] fp32 in [0, 1); values outside count as the nearest
+ *   settings     one value for all rows, or where the pointer beside it is not
+ *                NULL [rows] values on the device
+ *   tokens_dev   [rows] int32.  -1: all logits are minus infinity; or one is NaN
+ *                or infinite, or a setting on the device is not valid
+ *   probs_dev    [rows] fp32, may be NULL: the drawn token's share of the kept
+ *                weights; 0 or NaN in the cases of -1
+ * rows == 0 is a no-op.  Errors: INVALID_ARGUMENT (null pointer, ld < vocab,
+ * rows > W4A8_M_MAX, temperature negative or not finite, a NaN setting),
+ * UNSUPPORTED (vocab > W4A8_VOCAB_MAX), DEVICE. */
+#define W4A8_VOCAB_MAX (1 << 19)
+typedef struct {
+  float temperature;
+  int top_k;
+  float top_p;
+  float min_p;
+  const float* temperature_dev;
+  const int32_t* top_k_dev;
+  const float* top_p_dev;
+  const float* min_p_dev;
+} w4a8_sampling;
+w4a8_status w4a8_sample(const void* logits_dev, int logits_f32, int ld, int rows, int vocab,
+                        const float* u_dev, const w4a8_sampling* settings, int32_t* tokens_dev,
+                        float* probs_dev, void* stream);
+
+/* ------------------------------------------------------ pages of the cache
+ * Which page holds what, on the device: block tables as in w4a8_kv_view, and
+ * refs [num_pages] int32, how often the tables name each page (0: free; more than
+ * the entries where something else holds it too).  An entry outside
+ * [0, num_pages) names none; results have -1 there.  Every call writes new tables
+ * and counts beside the old ones, which it leaves as they are, so that a step can be
+ * taken back; the layers of a model share them, and repeat only
+ * w4a8_kv_copy_pages.  num_pages is at most W4A8_PAGES_MAX.
+ * Results do not depend on scheduling.
+ * Errors of all: INVALID_ARGUMENT (null pointer, bad size or stride, an output
+ * that is the input), UNSUPPORTED (page_size, sizes beyond these limits),
+ * BUFFER_TOO_SMALL, DEVICE. */
+#define W4A8_PAGES_MAX (1 << 22)
+
+/* Row i of the new table continues sequence parent[i] of the old one: its
+ * length, and the pages that hold tokens of it; where parent[i] == i all the pages
+ * of the row, also those without tokens yet.  parent outside [0, batch): an empty
+ * row.  So rows are copied (beams, several answers to one prompt), moved, kept
+ * and, where no new row continues them, freed.
+ *   parent_dev     [new_batch] int32
+ *   new_table_dev  [new_batch][new_table_ld], max_pages entries of each row
+ *   new_lens_dev   [new_batch], new_refs_dev [num_pages] */
+w4a8_status w4a8_kv_fork(const int32_t* block_table_dev, int block_table_ld, int max_pages,
+                         const int32_t* seq_lens_dev, int batch, const int32_t* refs_dev,
+                         int num_pages, int page_size, const int32_t* parent_dev, int new_batch,
+                         int32_t* new_table_dev, int new_table_ld, int32_t* new_lens_dev,
+                         int32_t* new_refs_dev, void* stream);
+
+/* Pages for the next tokens of every sequence: entries that they reach and that
+ * name no page get a free one, the lowest first, in the order of sequences and
+ * positions.  A page in which earlier tokens are followed by new ones is copied
+ * first if it is shared (refs > 1): the sequence gets a page of its own and the
+ * pair goes to src, dst for w4a8_kv_copy_pages.  All sequences that write a shared
+ * page copy it, except the last of them if nobody else holds it.
+ *   tokens_dev   [batch] int32 new tokens of each sequence, or NULL: `tokens` each
+ *   new_lens_dev [batch], the lengths with them
+ *   src_dev, dst_dev  [batch] int32: pairs in the order of sequences, then -1
+ *   counts_dev   [2] int32: the number of pairs, and that of entries that got no
+ *                page (they are -1: nothing is written there), because none was
+ *                free or the table has no room
+ *   workspace_dev  w4a8_kv_alloc_workspace_size bytes, 16-byte aligned, no
+ *                initialisation */
+size_t w4a8_kv_alloc_workspace_size(int batch, int num_pages);
+w4a8_status w4a8_kv_alloc(const int32_t* block_table_dev, int block_table_ld, int max_pages,
+                          const int32_t* seq_lens_dev, int batch, const int32_t* refs_dev,
+                          int num_pages, int page_size, const int32_t* tokens_dev, int tokens,
+                          int32_t* new_table_dev, int new_table_ld, int32_t* new_lens_dev,
+                          int32_t* new_refs_dev, int32_t* src_dev, int32_t* dst_dev,
+                          int32_t* counts_dev, void* workspace_dev, size_t workspace_bytes,
+                          void* stream);
+
+/* The pages in use moved to the front of the pool: of `live` ones the n-th that is
+ * at `live` or beyond takes the place of the n-th free one before.
+ *   place_dev    [num_pages] int32, where each page is now (for other tables that
+ *                name pages of the pool)
+ *   src_dev, dst_dev  [num_pages / 2] int32 pairs for w4a8_kv_copy_pages, then -1
+ *   counts_dev   [2] int32: the number of pairs, 0 */
+size_t w4a8_kv_compact_workspace_size(int num_pages);
+w4a8_status w4a8_kv_compact(const int32_t* block_table_dev, int block_table_ld, int max_pages,
+                            int batch, const int32_t* refs_dev, int num_pages,
+                            int32_t* new_table_dev, int new_table_ld, int32_t* new_refs_dev,
+                            int32_t* place_dev, int32_t* src_dev, int32_t* dst_dev,
+                            int32_t* counts_dev, void* workspace_dev, size_t workspace_bytes,
+                            void* stream);
+
+/* Page src[i] with its scales copied to page dst[i], for i < pairs, and
+ * i < count_dev[0] where count_dev is not NULL.  Pairs that name no page are
+ * skipped.  A page that is a source and a target, or a target twice, in one call
+ * has unspecified contents.  Arguments as in w4a8_kv_view.  UNSUPPORTED also for
+ * pages of more than 1 GiB. */
+w4a8_status w4a8_kv_copy_pages(int8_t* data_dev, uint16_t* scale_dev, long long page_stride,
+                               long long scale_stride, int num_pages, int page_size, int kv_heads,
+                               int head_dim, const int32_t* src_dev, const int32_t* dst_dev,
+                               int pairs, const int32_t* count_dev, void* stream);
+
 /* ------------------------------------------------------- measurement aid
  * Not part of the layer.  A read-only stream over `bytes` of device memory
  * (16-byte aligned, a multiple of 16) by `workgroups` x 512 threads, with

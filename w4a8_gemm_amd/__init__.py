@@ -15,7 +15,12 @@ torch.cuda.Stream of it to launch on (default: the current one); that the inputs
 are ready there is the caller's to arrange.
 
 Between the linears of a decoder: rms_norm_quant, silu_mul_quant, and a paged
-int8 KV cache (kv_cache, rope_table, rope_append, paged_attention).
+int8 KV cache (kv_cache, rope_table, rope_append, paged_attention).  Its pages are
+handed out, shared, freed and moved by kv_alloc, kv_fork, kv_compact and
+kv_copy_pages.
+
+At the end of a step: sample.  For drafted token trees: tree_mask,
+tree_attention, tree_accept, kv_keep.
 """
 from __future__ import annotations
 
@@ -41,6 +46,7 @@ GROUP_PER_CHANNEL = 0
 K_QUANTUM = 128
 N_QUANTUM = 16
 K_MAX = 131072
+M_MAX = 1 << 22
 
 STATUS = {
     0: "W4A8_OK",
@@ -77,12 +83,19 @@ class KvView(ctypes.Structure):
                 ("cu_q", ctypes.c_void_p), ("batch", ctypes.c_int), ("total_q", ctypes.c_int)]
 
 
+class Sampling(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("temperature_dev", ctypes.c_void_p),
+                ("top_k_dev", ctypes.c_void_p), ("top_p_dev", ctypes.c_void_p),
+                ("min_p_dev", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
                           "`python w4a8_gemm_amd/build.py` (or __graft_entry__.build())")
     lib = ctypes.CDLL(LIB_PATH)
-    P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    P, I, Z, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
     sig = {
         "w4a8_status_string": (ctypes.c_char_p, [I]),
         "w4a8_last_device_error": (ctypes.c_char_p, []),
@@ -103,6 +116,19 @@ def _load():
         "w4a8_rope_append": (I, [P, I, P, I, P, I, I, P, I, I, I, P, P, I, P]),
         "w4a8_paged_attention_workspace_size": (Z, [P, I, I, I]),
         "w4a8_paged_attention": (I, [P, I, I, P, I, I, ctypes.c_float, I, P, I, P, Z, P]),
+        "w4a8_rope_append_at": (I, [P, I, P, I, P, I, I, P, I, I, I, P, P, P, I, P]),
+        "w4a8_tree_mask": (I, [P, P, P, I, I, P, I, I, P, P]),
+        "w4a8_tree_attention_workspace_size": (Z, [P, I, I, I]),
+        "w4a8_tree_attention": (I, [P, I, I, P, P, I, I, I, I, ctypes.c_float, I, P, I, P, Z, P]),
+        "w4a8_tree_accept": (I, [P, P, P, P, P, I, I, P, I, I, P, P, P, P]),
+        "w4a8_kv_keep": (I, [P, P, I, I, P, P]),
+        "w4a8_sample": (I, [P, I, I, I, I, P, P, P, P, P]),
+        "w4a8_kv_fork": (I, [P, I, I, P, I, P, I, I, P, I, P, I, P, P, P]),
+        "w4a8_kv_alloc_workspace_size": (Z, [I, I]),
+        "w4a8_kv_alloc": (I, [P, I, I, P, I, P, I, I, P, I, P, I, P, P, P, P, P, P, Z, P]),
+        "w4a8_kv_compact_workspace_size": (Z, [I]),
+        "w4a8_kv_compact": (I, [P, I, I, I, P, I, P, I, P, P, P, P, P, P, Z, P]),
+        "w4a8_kv_copy_pages": (I, [P, P, L, L, I, I, I, I, P, P, I, P, P]),
         "w4a8_gemm_noalloc": (I, [P, I, P, I, P, I, I, I, P, I, P, I, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -506,10 +532,9 @@ def rope_table(max_pos: int, rotary_dim: int, base: float = 10000.0, scaling: st
     return torch.cat([angle.cos(), angle.sin()], dim=1).float().to(device)
 
 
-def _kv_view(cache, scale, block_table, seq_lens, cu_q, q):
-    """The C view of a cache and a batch for the new tokens of q, its tensors
-    checked."""
-    total_q, dev = q.shape[0], q.get_device()
+def _cache(cache, scale, dev):
+    """Check a paged cache on CUDA device `dev`; returns (pages, heads, page
+    size, head dim)."""
     if cache.dtype is not torch.int8 or cache.dim() != 5 or cache.shape[1] != 2:
         raise ValueError("cache: expected an int8 CUDA tensor [pages, 2, kv_heads, page_size, head_dim]")
     pages, _, heads, page, dim = cache.shape
@@ -519,13 +544,21 @@ def _kv_view(cache, scale, block_table, seq_lens, cu_q, q):
             or scale.stride()[1:] != (heads, 1):
         raise ValueError(f"scale: expected a float16 CUDA tensor [{pages}, 2, {heads}], "
                          "contiguous within a page")
-    if block_table.dtype is not torch.int32 or block_table.dim() != 2 \
-            or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
-        raise ValueError("block_table: expected an int32 CUDA tensor [batch, pages of a sequence]")
     if cache.get_device() != dev:
         raise _elsewhere("cache", cache, dev)
     if scale.get_device() != dev:
         raise _elsewhere("scale", scale, dev)
+    return pages, heads, page, dim
+
+
+def _kv_view(cache, scale, block_table, seq_lens, cu_q, q):
+    """The C view of a cache and a batch for the new tokens of q, its tensors
+    checked."""
+    total_q, dev = q.shape[0], q.get_device()
+    pages, heads, page, dim = _cache(cache, scale, dev)
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2 \
+            or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+        raise ValueError("block_table: expected an int32 CUDA tensor [batch, pages of a sequence]")
     if block_table.get_device() != dev:
         raise _elsewhere("block_table", block_table, dev)
     batch, max_pages = block_table.shape
@@ -564,11 +597,13 @@ def _heads(name, t, dev, tokens=None, heads=None, dim=None):
 
 @_on_device
 def rope_append(q, k, v, cos_sin, cache, scale, block_table, seq_lens, cu_q=None,
-                interleaved: bool = False, out=None, stream=None):
+                interleaved: bool = False, out=None, stream=None, positions=None):
     """Rotate q [tokens, heads, dim] and k by position and append k and v
     [tokens, kv_heads, dim] to the paged cache; returns the rotated q (a new
     tensor, or `out`, which may be q).  cos_sin [max_pos, rotary_dim] is
-    rope_table()'s, or None for no rotation.  See w4a8_rope_append."""
+    rope_table()'s, or None for no rotation.  positions, int32 [tokens], are the
+    angles' where they differ from the tokens' places in the cache (drafted
+    trees).  See w4a8_rope_append."""
     dev = q.get_device()
     tokens, heads, dim = q.shape
     view = _kv_view(cache, scale, block_table, seq_lens, cu_q, q)
@@ -587,6 +622,14 @@ def rope_append(q, k, v, cos_sin, cache, scale, block_table, seq_lens, cu_q=None
         out, ldo = _empty((tokens, heads, dim), torch.float16, q.device, stream), heads * dim
     else:
         ldo = _heads("out", out, dev, tokens, heads, dim)
+    if positions is not None:
+        _vector("positions", positions, torch.int32, dev, tokens)
+        _check(lib.w4a8_rope_append_at(
+            q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, heads,
+            cos_sin.data_ptr() if cos_sin is not None else None, rotary, max_pos, int(interleaved),
+            positions.data_ptr(), ctypes.byref(view), out.data_ptr(), ldo, _stream_of(q, stream)),
+            "w4a8_rope_append_at")
+        return out
     _check(lib.w4a8_rope_append(
         q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, heads,
         cos_sin.data_ptr() if cos_sin is not None else None, rotary, max_pos, int(interleaved),
@@ -629,6 +672,273 @@ def paged_attention(q, cache, scale_kv, block_table, seq_lens, cu_q=None, max_q:
         workspace.numel() * workspace.element_size() if workspace is not None else 0,
         _stream_of(q, stream)), "w4a8_paged_attention")
     return out
+
+
+def _tree(parents, seq_lens, cu_q, dev):
+    """Check a batch of drafted tokens; returns (tokens, batch)."""
+    tokens = parents.shape[0] if parents.dim() == 1 else -1
+    _vector("parents", parents, torch.int32, dev, tokens)
+    batch = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    _vector("seq_lens", seq_lens, torch.int32, dev, batch)
+    if cu_q is not None:
+        _vector("cu_q", cu_q, torch.int32, dev, batch + 1)
+    elif tokens != batch:
+        raise ValueError(f"without cu_q each of the {batch} sequences has one node, got {tokens}")
+    return tokens, batch
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _mask(mask, dev, tokens):
+    if mask.dtype is not torch.int32 or mask.dim() != 2 or mask.shape[0] != tokens or mask.shape[1] < 1 \
+            or (mask.stride(1) != 1 and mask.shape[1] > 1):
+        raise ValueError(f"mask: expected an int32 CUDA tensor [{tokens}, words] with contiguous rows")
+    if mask.get_device() != dev or dev < 0:
+        raise _elsewhere("mask", mask, dev)
+    return _ld(mask)
+
+
+@_on_device
+def tree_mask(parents, seq_lens, cu_q=None, max_q: int | None = None, mask=None, positions=None, stream=None):
+    """(mask int32 [tokens, ceil(max_q / 32)], positions int32 [tokens]) of
+    drafted trees: parents int32 [tokens] holds each node's parent within its
+    sequence, -1 for none.  max_q bounds the nodes of a sequence (default: all
+    of them).  See w4a8_tree_mask."""
+    dev = parents.get_device()
+    tokens, batch = _tree(parents, seq_lens, cu_q, dev)
+    if mask is not None:
+        ld = _mask(mask, dev, tokens)
+    if positions is not None:
+        _vector("positions", positions, torch.int32, dev, tokens)
+    if mask is None:
+        words = max(1, -(-(tokens if max_q is None else min(max_q, tokens)) // 32))
+        mask, ld = _empty((tokens, words), torch.int32, parents.device, stream), words
+    if positions is None:
+        positions = _empty((tokens,), torch.int32, parents.device, stream)
+    _check(lib.w4a8_tree_mask(parents.data_ptr(), seq_lens.data_ptr(), _ptr(cu_q), batch, tokens, mask.data_ptr(),
+                              ld, mask.shape[1], positions.data_ptr(), _stream_of(parents, stream)),
+           "w4a8_tree_mask")
+    return mask, positions
+
+
+@_on_device
+def tree_attention(q, cache, scale_kv, block_table, seq_lens, mask, cu_q=None, max_q: int | None = None,
+                   max_len: int | None = None, scale: float | None = None, window: int = 0, out=None,
+                   workspace=None, stream=None):
+    """Attention of drafted tokens q [tokens, heads, dim] over the paged int8
+    cache, which holds them already: all positions before the sequence's drafted
+    tokens, and of these the ones that mask (tree_mask()'s) names.  Other
+    arguments as paged_attention's.  See w4a8_tree_attention."""
+    dev = q.get_device()
+    tokens, heads, dim = q.shape
+    view = _kv_view(cache, scale_kv, block_table, seq_lens, cu_q, q)
+    ldq = _heads("q", q, dev, tokens, None, view.head_dim)
+    ld_mask = _mask(mask, dev, tokens)
+    if out is None:
+        out, ldo = _empty((tokens, heads, dim), torch.float16, q.device, stream), heads * dim
+    else:
+        ldo = _heads("out", out, dev, tokens, heads, dim)
+    if max_len is None:
+        max_len = view.max_pages * view.page_size
+    if max_q is None:
+        max_q = 1 if cu_q is None else tokens
+    if max_q > INT_MAX or max_len > INT_MAX or window > INT_MAX:
+        max_q, max_len, window = min(max_q, INT_MAX), min(max_len, INT_MAX), min(window, INT_MAX)
+    need = lib.w4a8_tree_attention_workspace_size(ctypes.byref(view), heads, max_q, max_len)
+    if need and workspace is None:
+        workspace = _empty(need, torch.uint8, q.device, stream, returned=False)
+    elif workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace: expected a contiguous CUDA tensor on device {dev}")
+    _check(lib.w4a8_tree_attention(
+        q.data_ptr(), ldq, heads, ctypes.byref(view), mask.data_ptr(), ld_mask, mask.shape[1], max_q, max_len,
+        dim ** -0.5 if scale is None else scale, window, out.data_ptr(), ldo, _ptr(workspace),
+        workspace.numel() * workspace.element_size() if workspace is not None else 0,
+        _stream_of(q, stream)), "w4a8_tree_attention")
+    return out
+
+
+@_on_device
+def tree_accept(drafted, parents, sampled, seq_lens, cu_q=None, max_q: int | None = None, stream=None):
+    """The nodes of drafted trees that sampled tokens confirm, all int32: (path
+    [batch, max_q] nodes in order, then -1, count [batch], tokens [batch] drawn
+    after the last of them, seq_lens [batch] without the others).  max_q bounds the
+    nodes of a path (default: all of them).  See w4a8_tree_accept."""
+    dev = drafted.get_device()
+    if dev < 0:
+        raise _elsewhere("drafted", drafted, dev)
+    tokens, batch = _tree(parents, seq_lens, cu_q, dev)
+    _vector("drafted", drafted, torch.int32, dev, tokens)
+    _vector("sampled", sampled, torch.int32, dev, tokens)
+    most = max(1, tokens if max_q is None else min(max_q, tokens))
+    new = lambda *shape: _empty(shape, torch.int32, drafted.device, stream)
+    path, count, following, lens = new(batch, most), new(batch), new(batch), new(batch)
+    _check(lib.w4a8_tree_accept(drafted.data_ptr(), parents.data_ptr(), sampled.data_ptr(), seq_lens.data_ptr(),
+                                _ptr(cu_q), batch, tokens, path.data_ptr(), most, most, count.data_ptr(),
+                                following.data_ptr(), lens.data_ptr(), _stream_of(drafted, stream)),
+           "w4a8_tree_accept")
+    return path, count, following, lens
+
+
+@_on_device
+def kv_keep(cache, scale, block_table, seq_lens, path, count, cu_q=None, stream=None):
+    """Keys and values of confirmed nodes (tree_accept()'s path and count) moved
+    to the places behind their sequence's certain tokens, in place; seq_lens and
+    cu_q are those that the nodes were appended with.  See w4a8_kv_keep."""
+    dev = cache.get_device()
+    if dev < 0:
+        raise _elsewhere("cache", cache, dev)
+    view = _kv_view(cache, scale, block_table, seq_lens, cu_q, path)
+    batch = view.batch
+    if path.dtype is not torch.int32 or path.dim() != 2 or path.shape[0] != batch or path.shape[1] < 1 \
+            or (path.stride(1) != 1 and path.shape[1] > 1):
+        raise ValueError(f"path: expected an int32 CUDA tensor [{batch}, nodes] with contiguous rows")
+    if path.get_device() != dev:
+        raise _elsewhere("path", path, dev)
+    _vector("count", count, torch.int32, dev, batch)
+    if cu_q is not None:
+        view.total_q = M_MAX             # not known here, and only a bound
+    _check(lib.w4a8_kv_keep(ctypes.byref(view), path.data_ptr(), _ld(path), path.shape[1], count.data_ptr(),
+                            _stream_of(cache, stream)), "w4a8_kv_keep")
+
+
+@_on_device
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, probs=None, stream=None):
+    """A token for each row of logits [rows, vocab] (float16 or float32) from the
+    random numbers u, float32 [rows] in [0, 1): returns (tokens int32 [rows], probs
+    float32 [rows], the share of the kept weights that each token has).  Settings
+    are numbers, or CUDA tensors of one value a row (float32, top_k int32);
+    temperature 0 takes the largest logit.  See w4a8_sample."""
+    dev = logits.get_device()
+    f32 = logits.dtype is torch.float32
+    _rows("logits", logits, torch.float32 if f32 else torch.float16, dev)
+    rows, vocab = logits.shape
+    _vector("u", u, torch.float32, dev, rows)
+    s = Sampling()
+    for name, value, kind in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                              ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if isinstance(value, torch.Tensor):
+            _vector(name, value, kind, dev, rows)
+            setattr(s, name + "_dev", value.data_ptr())
+        elif kind is torch.int32:
+            s.top_k = max(0, min(value, INT_MAX))
+        else:
+            setattr(s, name, value)
+    if tokens is None:
+        tokens = _empty((rows,), torch.int32, logits.device, stream)
+    else:
+        _vector("tokens", tokens, torch.int32, dev, rows)
+    if probs is None:
+        probs = _empty((rows,), torch.float32, logits.device, stream)
+    else:
+        _vector("probs", probs, torch.float32, dev, rows)
+    _check(lib.w4a8_sample(logits.data_ptr(), int(f32), _ld(logits), rows, vocab, u.data_ptr(), ctypes.byref(s),
+                           tokens.data_ptr(), probs.data_ptr(), _stream_of(logits, stream)), "w4a8_sample")
+    return tokens, probs
+
+
+def _table(block_table, dev):
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.shape[1] < 1 \
+            or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+        raise ValueError("block_table: expected an int32 CUDA tensor [batch, pages of a sequence]")
+    if block_table.get_device() != dev or dev < 0:
+        raise _elsewhere("block_table", block_table, dev)
+    return (*block_table.shape, _ld(block_table))
+
+
+def _pool_refs(refs, dev):
+    pages = refs.shape[0] if refs.dim() == 1 else -1
+    _vector("refs", refs, torch.int32, dev, pages)
+    return _int("pages", pages)
+
+
+@_on_device
+def kv_fork(block_table, seq_lens, refs, parent, page_size: int, stream=None):
+    """(block_table, seq_lens, refs) in which row i continues sequence parent[i]
+    (int32 [rows]; -1: an empty row) and pages without a row are free.  refs,
+    int32 [pages], counts how often tables name each page.  The arguments stay as
+    they are.  See w4a8_kv_fork."""
+    dev = block_table.get_device()
+    batch, width, ld = _table(block_table, dev)
+    _vector("seq_lens", seq_lens, torch.int32, dev, batch)
+    pages = _pool_refs(refs, dev)
+    rows = parent.shape[0] if parent.dim() == 1 else -1
+    _vector("parent", parent, torch.int32, dev, rows)
+    new = lambda *shape: _empty(shape, torch.int32, block_table.device, stream)
+    table, lens, counts = new(rows, width), new(rows), new(pages)
+    _check(lib.w4a8_kv_fork(block_table.data_ptr(), ld, width, seq_lens.data_ptr(), batch, refs.data_ptr(), pages,
+                            page_size, parent.data_ptr(), rows, table.data_ptr(), width, lens.data_ptr(),
+                            counts.data_ptr(), _stream_of(block_table, stream)), "w4a8_kv_fork")
+    return table, lens, counts
+
+
+@_on_device
+def kv_alloc(block_table, seq_lens, refs, tokens, page_size: int, stream=None):
+    """Pages for the next tokens (a number, or int32 [batch]) of each sequence:
+    (block_table, seq_lens with them, refs, src, dst, counts).  Pages src[i] are to
+    be copied to dst[i], for i < counts[0] (kv_copy_pages()); counts[1] entries got
+    no page.  The arguments stay as they are.  See w4a8_kv_alloc."""
+    dev = block_table.get_device()
+    batch, width, ld = _table(block_table, dev)
+    _vector("seq_lens", seq_lens, torch.int32, dev, batch)
+    pages = _pool_refs(refs, dev)
+    each = isinstance(tokens, torch.Tensor)
+    if each:
+        _vector("tokens", tokens, torch.int32, dev, batch)
+    else:
+        _int("tokens", tokens)
+    new = lambda *shape: _empty(shape, torch.int32, block_table.device, stream)
+    table, lens, owners, src, dst, counts = new(batch, width), new(batch), new(pages), new(batch), new(batch), new(2)
+    need = lib.w4a8_kv_alloc_workspace_size(batch, pages)
+    workspace = _empty(need, torch.uint8, block_table.device, stream, returned=False)
+    _check(lib.w4a8_kv_alloc(block_table.data_ptr(), ld, width, seq_lens.data_ptr(), batch, refs.data_ptr(), pages,
+                             page_size, tokens.data_ptr() if each else None, 0 if each else tokens,
+                             table.data_ptr(), width, lens.data_ptr(), owners.data_ptr(), src.data_ptr(),
+                             dst.data_ptr(), counts.data_ptr(), workspace.data_ptr(), need,
+                             _stream_of(block_table, stream)), "w4a8_kv_alloc")
+    return table, lens, owners, src, dst, counts
+
+
+@_on_device
+def kv_compact(block_table, refs, stream=None):
+    """The pages in use at the front of the pool: (block_table, refs, place, src,
+    dst, counts).  Pages src[i] are to be copied to dst[i], for i < counts[0]
+    (kv_copy_pages()); place [pages] says where each page is then.  The arguments
+    stay as they are.  See w4a8_kv_compact."""
+    dev = block_table.get_device()
+    batch, width, ld = _table(block_table, dev)
+    pages = _pool_refs(refs, dev)
+    new = lambda *shape: _empty(shape, torch.int32, block_table.device, stream)
+    moves = max(1, pages // 2)
+    table, owners, place, src, dst, counts = new(batch, width), new(pages), new(pages), new(moves), new(moves), new(2)
+    need = lib.w4a8_kv_compact_workspace_size(pages)
+    workspace = _empty(need, torch.uint8, block_table.device, stream, returned=False)
+    _check(lib.w4a8_kv_compact(block_table.data_ptr(), ld, width, batch, refs.data_ptr(), pages, table.data_ptr(),
+                               width, owners.data_ptr(), place.data_ptr(), src.data_ptr(), dst.data_ptr(),
+                               counts.data_ptr(), workspace.data_ptr(), need, _stream_of(block_table, stream)),
+           "w4a8_kv_compact")
+    return table, owners, place, src, dst, counts
+
+
+@_on_device
+def kv_copy_pages(cache, scale, src, dst, count=None, stream=None):
+    """Pages src[i] of a cache copied with their scales to dst[i] (int32), in
+    place, for all i or those below count[0] (int32, on the device).  See
+    w4a8_kv_copy_pages."""
+    dev = cache.get_device()
+    if dev < 0:
+        raise _elsewhere("cache", cache, dev)
+    pages, heads, page, dim = _cache(cache, scale, dev)
+    pairs = src.shape[0] if src.dim() == 1 else -1
+    _vector("src", src, torch.int32, dev, pairs)
+    _vector("dst", dst, torch.int32, dev, pairs)
+    if count is not None and (count.dtype is not torch.int32 or count.numel() < 1 or count.get_device() != dev):
+        raise ValueError(f"count: expected an int32 CUDA tensor on device {dev}")
+    _check(lib.w4a8_kv_copy_pages(
+        cache.data_ptr(), scale.data_ptr(), cache.stride(0) if pages > 1 else 2 * heads * page * dim,
+        scale.stride(0) if pages > 1 else 2 * heads, pages, page, heads, dim, src.data_ptr(), dst.data_ptr(), pairs,
+        _ptr(count), _stream_of(cache, stream)), "w4a8_kv_copy_pages")
 
 
 @_on_device

@@ -48,10 +48,10 @@ def build(verbose: bool = False) -> str:
     steps = []
     for src in ("fused.hip", "skinny.hip", "tiled.hip", "quant_act.hip", "w4a16.hip",
                 "probe.hip", "scratch.hip", "row_quant.hip", "kv_append.hip", "paged_attn.hip",
-                "paged_attn_tile.hip"):
+                "paged_attn_tile.hip", "tree_attn.hip", "tree.hip", "sample.hip", "kv_pages.hip"):
         obj = os.path.join(BUILD, src + ".o")
         steps.append((obj, [HIPCC, *HIP_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]))
-    for src in ("api.cpp", "configs.cpp", "decoder_api.cpp"):
+    for src in ("api.cpp", "configs.cpp", "decoder_api.cpp", "verify_api.cpp"):
         obj = os.path.join(BUILD, src + ".o")
         steps.append((obj, [HIPCC, *HIP_FLAGS, "-x", "hip", "-c", os.path.join(CSRC, src),
                             "-o", obj]))

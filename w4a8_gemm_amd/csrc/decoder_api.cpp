@@ -7,61 +7,12 @@
 #include <cstdint>
 
 #include "../../include/w4a8.h"
+#include "decoder_checks.h"
 #include "decoder_kernels.h"
 
 using namespace w4a8;
 
 namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// rows of `cols` fp16 values read and written 16 bytes at a time
-bool rows_ok(const void* p, int ld, long cols) {
-  return p && aligned16(p) && ld >= cols && ld % 8 == 0;
-}
-
-// The view's sizes and pointers; on success fills `a`.  A view of an empty
-// batch or of no new tokens is accepted with null pointers (`a` is then
-// not used).
-w4a8_status check_view(const w4a8_kv_view* v, KvArgs* a) {
-  if (!v) return W4A8_ERR_INVALID_ARGUMENT;
-  if (v->num_pages < 1 || v->kv_heads < 1 || v->batch < 0 || v->total_q < 0 || v->max_pages < 1 ||
-      v->block_table_ld < v->max_pages || v->batch > W4A8_M_MAX || v->total_q > W4A8_M_MAX)
-    return W4A8_ERR_INVALID_ARGUMENT;
-  if (v->head_dim < 16 || v->head_dim > W4A8_HEAD_DIM_MAX || v->head_dim % 16 ||
-      v->kv_heads > W4A8_HEADS_MAX)
-    return W4A8_ERR_UNSUPPORTED;
-  int shift = 4;
-  while (shift < 10 && (1 << shift) < v->page_size) ++shift;
-  if (v->page_size != 1 << shift) return W4A8_ERR_UNSUPPORTED;
-  if (long(v->max_pages) << shift > 2147483647l - v->page_size) return W4A8_ERR_INVALID_ARGUMENT;
-  // without cu_q every sequence brings one token
-  if (!v->cu_q_dev && v->total_q != v->batch) return W4A8_ERR_INVALID_ARGUMENT;
-  const long block = long(v->page_size) * v->head_dim;
-  const long page = 2l * v->kv_heads * block;
-  if (v->page_stride < page || v->page_stride % 16 || v->scale_stride < 2l * v->kv_heads)
-    return W4A8_ERR_INVALID_ARGUMENT;
-  if (v->batch == 0 || v->total_q == 0) return W4A8_OK;
-  if (!v->data_dev || !v->scale_dev || !v->block_table_dev || !v->seq_lens_dev)
-    return W4A8_ERR_INVALID_ARGUMENT;
-  if (!aligned16(v->data_dev)) return W4A8_ERR_INVALID_ARGUMENT;
-  a->data = v->data_dev;
-  a->scale = v->scale_dev;
-  a->page_stride = long(v->page_stride);
-  a->scale_stride = long(v->scale_stride);
-  a->num_pages = v->num_pages;
-  a->kv_heads = v->kv_heads;
-  a->dim = v->head_dim;
-  a->page_shift = shift;
-  a->table = v->block_table_dev;
-  a->table_ld = v->block_table_ld;
-  a->max_pages = v->max_pages;
-  a->lens = v->seq_lens_dev;
-  a->cu_q = v->cu_q_dev;
-  a->batch = v->batch;
-  a->total_q = v->total_q;
-  return W4A8_OK;
-}
 
 // What the attention launches for a batch: the kernel of 16-row tiles
 // (waves == 0) or the one of 32 rows a wave, and the split of the keys.
@@ -119,20 +70,14 @@ AttnPlan plan_attn(const KvArgs& kv, int q_heads, int max_q, int max_len) {
   return pl;
 }
 
-w4a8_status check_heads(const KvArgs& kv, int q_heads) {
-  if (q_heads < 1) return W4A8_ERR_INVALID_ARGUMENT;
-  if (q_heads % kv.kv_heads || q_heads > W4A8_HEADS_MAX) return W4A8_ERR_UNSUPPORTED;
-  if (long(kv.total_q) * q_heads > 2147483647l) return W4A8_ERR_UNSUPPORTED;
-  return W4A8_OK;
-}
-
 }  // namespace
 
-extern "C" w4a8_status w4a8_rope_append(const uint16_t* q_dev, int ldq, const uint16_t* k_dev,
-                                        int ldk, const uint16_t* v_dev, int ldv, int q_heads,
-                                        const float* cos_sin_dev, int rotary_dim, int max_pos,
-                                        int interleaved, const w4a8_kv_view* view,
-                                        uint16_t* q_out_dev, int ldqo, void* stream) {
+extern "C" w4a8_status w4a8_rope_append_at(const uint16_t* q_dev, int ldq, const uint16_t* k_dev,
+                                           int ldk, const uint16_t* v_dev, int ldv, int q_heads,
+                                           const float* cos_sin_dev, int rotary_dim, int max_pos,
+                                           int interleaved, const int32_t* positions_dev,
+                                           const w4a8_kv_view* view, uint16_t* q_out_dev, int ldqo,
+                                           void* stream) {
   AppendParams p;
   w4a8_status st = check_view(view, &p.kv);
   if (st != W4A8_OK) return st;
@@ -162,7 +107,17 @@ extern "C" w4a8_status w4a8_rope_append(const uint16_t* q_dev, int ldq, const ui
   p.rotary = rotary_dim;
   p.max_pos = max_pos;
   p.interleaved = interleaved;
+  p.positions = positions_dev;
   return device_status(launch_rope_append(p, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" w4a8_status w4a8_rope_append(const uint16_t* q_dev, int ldq, const uint16_t* k_dev,
+                                        int ldk, const uint16_t* v_dev, int ldv, int q_heads,
+                                        const float* cos_sin_dev, int rotary_dim, int max_pos,
+                                        int interleaved, const w4a8_kv_view* view,
+                                        uint16_t* q_out_dev, int ldqo, void* stream) {
+  return w4a8_rope_append_at(q_dev, ldq, k_dev, ldk, v_dev, ldv, q_heads, cos_sin_dev, rotary_dim,
+                             max_pos, interleaved, nullptr, view, q_out_dev, ldqo, stream);
 }
 
 extern "C" size_t w4a8_paged_attention_workspace_size(const w4a8_kv_view* view, int q_heads,

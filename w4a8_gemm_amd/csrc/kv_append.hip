@@ -30,6 +30,8 @@ namespace w4a8 {
 namespace {
 
 using namespace dev;
+using kv::codes4;
+using kv::rescale4;
 
 constexpr int kThreads = 256;
 
@@ -99,27 +101,6 @@ __device__ __forceinline__ void rotate16(float (&v)[16], const Turn& t, bool int
   }
 }
 
-// four fp32 values to int8 codes in one dword
-__device__ __forceinline__ uint32_t codes4(const float* v, float r) {
-  uint32_t b[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float y = __builtin_amdgcn_fmed3f(v[i] * r, -127.0f, 127.0f);
-    b[i] = __builtin_bit_cast(uint32_t, y + 12582912.0f);
-  }
-  const uint32_t p01 = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
-  const uint32_t p23 = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
-  return p01 | p23;
-}
-
-// the dword's four codes under a scale `ratio` times as fine
-__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
-  float v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = float(int8_t(uint8_t(w >> (8 * i))));
-  return codes4(v, ratio);
-}
-
 // WPB waves own a block (1: the block belongs to one wave, 4 blocks per
 // workgroup; 4: to the workgroup).  Up to kHeld items a thread stay in
 // registers from the search for their largest value to their quantization;
@@ -170,7 +151,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int unit) {
     return item_of(i - *t * per_token, rotary, inter);
   };
   auto turn = [&](float (&v)[16], const Item& it, int t) {
-    if (it.pair >= 0) rotate16(v, turn_of(p, it, begin + t), inter);
+    if (it.pair >= 0) rotate16(v, turn_of(p, it, p.positions ? p.positions[token0 + t] : begin + t), inter);
   };
   // the items' loads go out before the page's number and old scale are there
   Raw raw[kHeld];
@@ -286,10 +267,16 @@ __device__ __forceinline__ void rotate_queries(const AppendParams& p, long index
     if (h0 + h < p.q_heads) raw[h] = load_raw(p.q + t * p.ldq + long(h0 + h) * kv.dim, it);
   Turn turn;
   if (it.pair >= 0) {
-    int b = int(t), nth = 0;
-    if (kv.cu_q) b = kv::owner(int(t), kv.batch, [&](int i) { return kv.cu_q[i]; }, &nth);
-    const kv::Seq s = kv::seq_of(kv, b);
-    turn = turn_of(p, it, s.len - s.hi + int(t));
+    int pos;
+    if (p.positions) {
+      pos = p.positions[t];
+    } else {
+      int b = int(t), nth = 0;
+      if (kv.cu_q) b = kv::owner(int(t), kv.batch, [&](int i) { return kv.cu_q[i]; }, &nth);
+      const kv::Seq s = kv::seq_of(kv, b);
+      pos = s.len - s.hi + int(t);
+    }
+    turn = turn_of(p, it, pos);
   }
 #pragma unroll
   for (int h = 0; h < HEADS; ++h) {

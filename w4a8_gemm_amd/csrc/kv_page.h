@@ -76,5 +76,26 @@ static __device__ __forceinline__ int scalar_load(const int32_t* p) {
   return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t(p));
 }
 
+// four fp32 values to int8 codes in one dword
+static __device__ __forceinline__ uint32_t codes4(const float* v, float r) {
+  uint32_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float y = __builtin_amdgcn_fmed3f(v[i] * r, -127.0f, 127.0f);
+    b[i] = __builtin_bit_cast(uint32_t, y + 12582912.0f);
+  }
+  const uint32_t p01 = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
+  const uint32_t p23 = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+  return p01 | p23;
+}
+
+// the dword's four codes under a scale `ratio` times as fine
+static __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = float(int8_t(uint8_t(w >> (8 * i))));
+  return codes4(v, ratio);
+}
+
 }  // namespace kv
 }  // namespace w4a8

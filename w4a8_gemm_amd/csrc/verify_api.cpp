@@ -1,0 +1,360 @@
+// C ABI entry points of the operators that verify and end a decoding step:
+// argument validation (host only, before any HIP call) and launch plans.
+#include <hip/hip_runtime_api.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/w4a8.h"
+#include "decoder_checks.h"
+#include "decoder_kernels.h"
+#include "verify_kernels.h"
+
+using namespace w4a8;
+
+namespace {
+
+constexpr long kIntMax = 2147483647l;
+
+// What tree_attention launches for a batch: row tiles of 16 a workgroup, and the
+// split of the keys.
+struct TreePlan {
+  int tiles;
+  int splits, chunk;
+  long wgs;
+  size_t ml_bytes, workspace;
+};
+
+constexpr long kComputeUnits = 256;
+constexpr int kMaxSplits = 256;
+
+TreePlan plan_tree(const KvArgs& kv, int q_heads, int max_q, int max_len) {
+  TreePlan pl;
+  const int group = q_heads / kv.kv_heads;
+  const long rows = long(kv.cu_q ? max_q : 1) * group;
+  pl.tiles = rows <= 16 ? 1 : rows <= 32 || kv.dim > 128 ? 2 : 4;
+  const long units = attn_tiles(kv, group, 16 * pl.tiles) * kv.kv_heads;
+  const long rows_all = long(kv.total_q) * q_heads;
+  const long least = 256;
+  const double keys = double(units) * max_len;
+  double want = std::max(keys / double(4 * kComputeUnits), double(max_len) / kMaxSplits);
+  if (rows_all > kMaxWgs256) want = max_len;
+  const long chunk = std::max(1l, (long(want) + least) / least) * least;
+  const long splits = std::max(1l, (max_len + chunk - 1) / chunk);
+  pl.splits = int(splits);
+  pl.chunk = int(std::min(chunk, 1l << 30));
+  pl.wgs = units * splits;
+  const size_t parts = splits > 1 ? size_t(rows_all) * size_t(splits) : 0;
+  pl.ml_bytes = (parts * 8 + 255) / 256 * 256;
+  pl.workspace = parts > 0 ? pl.ml_bytes + parts * size_t(kv.dim) * 4 : 0;
+  return pl;
+}
+
+// A batch of drafted tokens.
+w4a8_status check_tree(const int32_t* parents, const int32_t* lens, const int32_t* cu_q, int batch,
+                       int total_q, TreeBatch* t) {
+  if (batch < 0 || total_q < 0 || batch > W4A8_M_MAX || total_q > W4A8_M_MAX)
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (!cu_q && total_q != batch) return W4A8_ERR_INVALID_ARGUMENT;
+  if (batch > 0 && !lens) return W4A8_ERR_INVALID_ARGUMENT;
+  if (batch > 0 && total_q > 0 && !parents) return W4A8_ERR_INVALID_ARGUMENT;
+  t->parents = parents;
+  t->lens = lens;
+  t->cu_q = cu_q;
+  t->batch = batch;
+  t->total_q = total_q;
+  return W4A8_OK;
+}
+
+// log2 of a page size, or -1
+int page_shift_of(int page_size) {
+  for (int shift = 4; shift <= 10; ++shift)
+    if (page_size == 1 << shift) return shift;
+  return -1;
+}
+
+// A table over a pool of pages, and where its successor goes.
+w4a8_status check_table(const int32_t* table, int table_ld, int max_pages, int batch, int new_batch,
+                        const int32_t* refs, int num_pages, int32_t* new_table, int new_ld,
+                        int32_t* new_refs, TableArgs* t) {
+  if (max_pages < 1 || batch < 0 || new_batch < 0 || num_pages < 1 || table_ld < max_pages ||
+      new_ld < max_pages || batch > W4A8_M_MAX || new_batch > W4A8_M_MAX)
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (!refs || !new_refs || refs == new_refs) return W4A8_ERR_INVALID_ARGUMENT;
+  if ((batch > 0 && !table) || (new_batch > 0 && !new_table) || (batch > 0 && table == new_table))
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (num_pages > kPageBlock * kPageBlocks) return W4A8_ERR_UNSUPPORTED;
+  if (long(std::max(batch, new_batch)) * max_pages > kIntMax) return W4A8_ERR_UNSUPPORTED;
+  t->table = table;
+  t->table_ld = table_ld;
+  t->max_pages = max_pages;
+  t->batch = batch;
+  t->refs = refs;
+  t->num_pages = num_pages;
+  t->new_table = new_table;
+  t->new_ld = new_ld;
+  t->new_refs = new_refs;
+  return W4A8_OK;
+}
+
+}  // namespace
+
+extern "C" w4a8_status w4a8_tree_mask(const int32_t* parents_dev, const int32_t* seq_lens_dev,
+                                      const int32_t* cu_q_dev, int batch, int total_q,
+                                      uint32_t* mask_dev, int mask_ld, int mask_words,
+                                      int32_t* positions_dev, void* stream) {
+  TreeMaskParams p;
+  const w4a8_status st = check_tree(parents_dev, seq_lens_dev, cu_q_dev, batch, total_q, &p.tree);
+  if (st != W4A8_OK) return st;
+  if (mask_words < 1 || mask_ld < mask_words) return W4A8_ERR_INVALID_ARGUMENT;
+  if (batch == 0 || total_q == 0) return W4A8_OK;
+  if (!mask_dev) return W4A8_ERR_INVALID_ARGUMENT;
+  p.mask = mask_dev;
+  p.mask_ld = mask_ld;
+  p.words = mask_words;
+  p.positions = positions_dev;
+  return device_status(launch_tree_mask(p, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" size_t w4a8_tree_attention_workspace_size(const w4a8_kv_view* view, int q_heads, int max_q,
+                                                     int max_len) {
+  KvArgs kv;
+  if (check_view(view, &kv) != W4A8_OK || view->batch == 0 || view->total_q == 0) return 0;
+  if (check_heads(kv, q_heads) != W4A8_OK || max_q < 0 || max_len < 0) return 0;
+  return plan_tree(kv, q_heads, max_q, max_len).workspace;
+}
+
+extern "C" w4a8_status w4a8_tree_attention(const uint16_t* q_dev, int ldq, int q_heads,
+                                           const w4a8_kv_view* view, const uint32_t* mask_dev,
+                                           int mask_ld, int mask_words, int max_q, int max_len,
+                                           float scale, int window, uint16_t* out_dev, int ldo,
+                                           void* workspace_dev, size_t workspace_bytes, void* stream) {
+  AttnParams p;
+  w4a8_status st = check_view(view, &p.kv);
+  if (st != W4A8_OK) return st;
+  if (max_q < 0 || max_len < 0 || window < 0 || !std::isfinite(scale) || mask_words < 1 ||
+      mask_ld < mask_words)
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (view->batch == 0 || view->total_q == 0) return W4A8_OK;
+  st = check_heads(p.kv, q_heads);
+  if (st != W4A8_OK) return st;
+  const long cols = long(q_heads) * p.kv.dim;
+  if (!mask_dev || !rows_ok(q_dev, ldq, cols) || !rows_ok(out_dev, ldo, cols))
+    return W4A8_ERR_INVALID_ARGUMENT;
+  const TreePlan pl = plan_tree(p.kv, q_heads, max_q, max_len);
+  if (pl.wgs > kMaxWgs256) return W4A8_ERR_UNSUPPORTED;
+  if (pl.workspace > 0) {
+    if (workspace_bytes < pl.workspace) return W4A8_ERR_BUFFER_TOO_SMALL;
+    if (!workspace_dev || !aligned16(workspace_dev)) return W4A8_ERR_INVALID_ARGUMENT;
+  }
+  p.q = q_dev;
+  p.out = out_dev;
+  p.ldq = ldq;
+  p.ldo = ldo;
+  p.q_heads = q_heads;
+  p.group = q_heads / p.kv.kv_heads;
+  p.scale_log2e = scale * 1.44269504f;
+  p.window = window;
+  p.splits = pl.splits;
+  p.chunk = pl.chunk;
+  p.part_ml = static_cast<float2*>(workspace_dev);
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace_dev) + (pl.workspace ? pl.ml_bytes : 0));
+  p.mask = mask_dev;
+  p.mask_ld = mask_ld;
+  p.mask_words = mask_words;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  st = device_status(launch_tree_attn(p, pl.tiles, s));
+  if (st != W4A8_OK || pl.splits == 1) return st;
+  return device_status(launch_attn_join(p, s));
+}
+
+extern "C" w4a8_status w4a8_tree_accept(const int32_t* drafted_dev, const int32_t* parents_dev,
+                                        const int32_t* sampled_dev, const int32_t* seq_lens_dev,
+                                        const int32_t* cu_q_dev, int batch, int total_q,
+                                        int32_t* path_dev, int path_ld, int max_path,
+                                        int32_t* count_dev, int32_t* tokens_dev,
+                                        int32_t* new_lens_dev, void* stream) {
+  AcceptParams p;
+  const w4a8_status st = check_tree(parents_dev, seq_lens_dev, cu_q_dev, batch, total_q, &p.tree);
+  if (st != W4A8_OK) return st;
+  if (max_path < 1 || path_ld < max_path) return W4A8_ERR_INVALID_ARGUMENT;
+  if (batch == 0) return W4A8_OK;
+  if ((total_q > 0 && (!drafted_dev || !sampled_dev)) || !path_dev || !count_dev || !tokens_dev ||
+      !new_lens_dev)
+    return W4A8_ERR_INVALID_ARGUMENT;
+  p.drafted = drafted_dev;
+  p.sampled = sampled_dev;
+  p.path = path_dev;
+  p.path_ld = path_ld;
+  p.max_path = max_path;
+  p.count = count_dev;
+  p.tokens = tokens_dev;
+  p.new_lens = new_lens_dev;
+  return device_status(launch_tree_accept(p, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" w4a8_status w4a8_kv_keep(const w4a8_kv_view* view, const int32_t* path_dev, int path_ld,
+                                    int max_path, const int32_t* count_dev, void* stream) {
+  KeepParams p;
+  const w4a8_status st = check_view(view, &p.kv);
+  if (st != W4A8_OK) return st;
+  if (max_path < 1 || path_ld < max_path) return W4A8_ERR_INVALID_ARGUMENT;
+  if (view->batch == 0 || view->total_q == 0) return W4A8_OK;
+  if (!path_dev || !count_dev) return W4A8_ERR_INVALID_ARGUMENT;
+  if (2l * view->batch * view->kv_heads > kIntMax - 4) return W4A8_ERR_UNSUPPORTED;
+  p.path = path_dev;
+  p.path_ld = path_ld;
+  p.max_path = max_path;
+  p.count = count_dev;
+  return device_status(launch_kv_keep(p, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" w4a8_status w4a8_sample(const void* logits_dev, int logits_f32, int ld, int rows, int vocab,
+                                   const float* u_dev, const w4a8_sampling* settings,
+                                   int32_t* tokens_dev, float* probs_dev, void* stream) {
+  if (rows < 0 || rows > W4A8_M_MAX || vocab < 1 || ld < vocab || !settings)
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (vocab > W4A8_VOCAB_MAX) return W4A8_ERR_UNSUPPORTED;
+  const w4a8_sampling& s = *settings;
+  if ((!s.temperature_dev && !(s.temperature >= 0.0f && std::isfinite(s.temperature))) ||
+      (!s.top_p_dev && std::isnan(s.top_p)) || (!s.min_p_dev && std::isnan(s.min_p)))
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return W4A8_OK;
+  if (!logits_dev || !u_dev || !tokens_dev) return W4A8_ERR_INVALID_ARGUMENT;
+  if (reinterpret_cast<uintptr_t>(logits_dev) % (logits_f32 ? 4 : 2)) return W4A8_ERR_INVALID_ARGUMENT;
+  SampleParams p;
+  p.logits = logits_dev;
+  p.f32 = logits_f32;
+  p.ld = ld;
+  p.rows = rows;
+  p.vocab = vocab;
+  p.u = u_dev;
+  p.s = s;
+  p.tokens = tokens_dev;
+  p.probs = probs_dev;
+  return device_status(launch_sample(p, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" w4a8_status w4a8_kv_fork(const int32_t* block_table_dev, int block_table_ld, int max_pages,
+                                    const int32_t* seq_lens_dev, int batch, const int32_t* refs_dev,
+                                    int num_pages, int page_size, const int32_t* parent_dev,
+                                    int new_batch, int32_t* new_table_dev, int new_table_ld,
+                                    int32_t* new_lens_dev, int32_t* new_refs_dev, void* stream) {
+  ForkParams p;
+  const w4a8_status st = check_table(block_table_dev, block_table_ld, max_pages, batch, new_batch, refs_dev,
+                                     num_pages, new_table_dev, new_table_ld, new_refs_dev, &p.t);
+  if (st != W4A8_OK) return st;
+  p.page_shift = page_shift_of(page_size);
+  if (p.page_shift < 0) return W4A8_ERR_UNSUPPORTED;
+  if (long(max_pages) << p.page_shift > kIntMax - page_size) return W4A8_ERR_INVALID_ARGUMENT;
+  if ((batch > 0 && !seq_lens_dev) || (new_batch > 0 && (!parent_dev || !new_lens_dev)) ||
+      (new_batch > 0 && seq_lens_dev == new_lens_dev))
+    return W4A8_ERR_INVALID_ARGUMENT;
+  p.lens = seq_lens_dev;
+  p.parent = parent_dev;
+  p.new_batch = new_batch;
+  p.new_lens = new_lens_dev;
+  return device_status(launch_kv_fork(p, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" size_t w4a8_kv_alloc_workspace_size(int batch, int num_pages) {
+  if (batch < 0 || batch > W4A8_M_MAX || num_pages < 1 || num_pages > kPageBlock * kPageBlocks) return 0;
+  return (2 * size_t(num_pages) + size_t(page_blocks(num_pages)) + 5 * size_t(batch)) * 4;
+}
+
+extern "C" w4a8_status w4a8_kv_alloc(const int32_t* block_table_dev, int block_table_ld, int max_pages,
+                                     const int32_t* seq_lens_dev, int batch, const int32_t* refs_dev,
+                                     int num_pages, int page_size, const int32_t* tokens_dev, int tokens,
+                                     int32_t* new_table_dev, int new_table_ld, int32_t* new_lens_dev,
+                                     int32_t* new_refs_dev, int32_t* src_dev, int32_t* dst_dev,
+                                     int32_t* counts_dev, void* workspace_dev, size_t workspace_bytes,
+                                     void* stream) {
+  AllocParams p;
+  const w4a8_status st = check_table(block_table_dev, block_table_ld, max_pages, batch, batch, refs_dev,
+                                     num_pages, new_table_dev, new_table_ld, new_refs_dev, &p.t);
+  if (st != W4A8_OK) return st;
+  p.page_shift = page_shift_of(page_size);
+  if (p.page_shift < 0) return W4A8_ERR_UNSUPPORTED;
+  if (long(max_pages) << p.page_shift > kIntMax - page_size || tokens < 0) return W4A8_ERR_INVALID_ARGUMENT;
+  if (!counts_dev || (batch > 0 && (!seq_lens_dev || !new_lens_dev || !src_dev || !dst_dev ||
+                                    seq_lens_dev == new_lens_dev)))
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < w4a8_kv_alloc_workspace_size(batch, num_pages)) return W4A8_ERR_BUFFER_TOO_SMALL;
+  if (!workspace_dev || !aligned16(workspace_dev)) return W4A8_ERR_INVALID_ARGUMENT;
+  p.lens = seq_lens_dev;
+  p.tokens_dev = tokens_dev;
+  p.tokens = tokens;
+  p.new_lens = new_lens_dev;
+  p.src = src_dev;
+  p.dst = dst_dev;
+  p.counts = counts_dev;
+  p.writers = static_cast<int32_t*>(workspace_dev);
+  p.final_row = p.writers + num_pages;
+  p.block_free = p.final_row + num_pages;
+  p.row_need = p.block_free + page_blocks(num_pages);
+  p.row_base = p.row_need + batch;
+  p.row_held = p.row_base + batch;
+  p.row_pair = p.row_held + batch;
+  p.row_over = p.row_pair + batch;
+  return device_status(launch_kv_alloc(p, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" size_t w4a8_kv_compact_workspace_size(int num_pages) {
+  if (num_pages < 1 || num_pages > kPageBlock * kPageBlocks) return 0;
+  return (size_t(num_pages) + size_t(page_blocks(num_pages))) * 4;
+}
+
+extern "C" w4a8_status w4a8_kv_compact(const int32_t* block_table_dev, int block_table_ld, int max_pages,
+                                       int batch, const int32_t* refs_dev, int num_pages,
+                                       int32_t* new_table_dev, int new_table_ld, int32_t* new_refs_dev,
+                                       int32_t* place_dev, int32_t* src_dev, int32_t* dst_dev,
+                                       int32_t* counts_dev, void* workspace_dev, size_t workspace_bytes,
+                                       void* stream) {
+  CompactParams p;
+  const w4a8_status st = check_table(block_table_dev, block_table_ld, max_pages, batch, batch, refs_dev,
+                                     num_pages, new_table_dev, new_table_ld, new_refs_dev, &p.t);
+  if (st != W4A8_OK) return st;
+  if (!place_dev || !counts_dev || (num_pages > 1 && (!src_dev || !dst_dev)))
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < w4a8_kv_compact_workspace_size(num_pages)) return W4A8_ERR_BUFFER_TOO_SMALL;
+  if (!workspace_dev || !aligned16(workspace_dev)) return W4A8_ERR_INVALID_ARGUMENT;
+  p.place = place_dev;
+  p.src = src_dev;
+  p.dst = dst_dev;
+  p.counts = counts_dev;
+  p.rank = static_cast<int32_t*>(workspace_dev);
+  p.block_live = p.rank + num_pages;
+  return device_status(launch_kv_compact(p, static_cast<hipStream_t>(stream)));
+}
+
+extern "C" w4a8_status w4a8_kv_copy_pages(int8_t* data_dev, uint16_t* scale_dev, long long page_stride,
+                                          long long scale_stride, int num_pages, int page_size,
+                                          int kv_heads, int head_dim, const int32_t* src_dev,
+                                          const int32_t* dst_dev, int pairs, const int32_t* count_dev,
+                                          void* stream) {
+  if (num_pages < 1 || kv_heads < 1 || pairs < 0) return W4A8_ERR_INVALID_ARGUMENT;
+  if (page_shift_of(page_size) < 0 || kv_heads > W4A8_HEADS_MAX || head_dim < 16 ||
+      head_dim > W4A8_HEAD_DIM_MAX || head_dim % 16)
+    return W4A8_ERR_UNSUPPORTED;
+  const long bytes = 2l * kv_heads * page_size * head_dim;
+  if (page_stride < bytes || page_stride % 16 || scale_stride < 2l * kv_heads)
+    return W4A8_ERR_INVALID_ARGUMENT;
+  if (bytes > 1l << 30) return W4A8_ERR_UNSUPPORTED;
+  if (pairs == 0) return W4A8_OK;
+  if (!data_dev || !scale_dev || !src_dev || !dst_dev || !aligned16(data_dev))
+    return W4A8_ERR_INVALID_ARGUMENT;
+  CopyParams p;
+  p.data = data_dev;
+  p.scale = scale_dev;
+  p.page_stride = long(page_stride);
+  p.scale_stride = long(scale_stride);
+  p.num_pages = num_pages;
+  p.page_bytes = int(bytes);
+  p.scales = 2 * kv_heads;
+  p.src = src_dev;
+  p.dst = dst_dev;
+  p.pairs = pairs;
+  p.count = count_dev;
+  return device_status(launch_kv_copy(p, static_cast<hipStream_t>(stream)));
+}
