@@ -687,6 +687,10 @@ def _tree(parents, seq_lens, cu_q, dev):
     return tokens, batch
 
 
+def _most_nodes(tokens, cu_q, max_q):
+    return 1 if cu_q is None else tokens if max_q is None else min(max_q, tokens)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -713,7 +717,7 @@ def tree_mask(parents, seq_lens, cu_q=None, max_q: int | None = None, mask=None,
     if positions is not None:
         _vector("positions", positions, torch.int32, dev, tokens)
     if mask is None:
-        words = max(1, -(-(tokens if max_q is None else min(max_q, tokens)) // 32))
+        words = max(1, -(-_most_nodes(tokens, cu_q, max_q) // 32))
         mask, ld = _empty((tokens, words), torch.int32, parents.device, stream), words
     if positions is None:
         positions = _empty((tokens,), torch.int32, parents.device, stream)
@@ -771,7 +775,7 @@ def tree_accept(drafted, parents, sampled, seq_lens, cu_q=None, max_q: int | Non
     tokens, batch = _tree(parents, seq_lens, cu_q, dev)
     _vector("drafted", drafted, torch.int32, dev, tokens)
     _vector("sampled", sampled, torch.int32, dev, tokens)
-    most = max(1, tokens if max_q is None else min(max_q, tokens))
+    most = max(1, _most_nodes(tokens, cu_q, max_q))
     new = lambda *shape: _empty(shape, torch.int32, drafted.device, stream)
     path, count, following, lens = new(batch, most), new(batch), new(batch), new(batch)
     _check(lib.w4a8_tree_accept(drafted.data_ptr(), parents.data_ptr(), sampled.data_ptr(), seq_lens.data_ptr(),

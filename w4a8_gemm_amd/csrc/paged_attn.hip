@@ -347,11 +347,13 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   int b = t, nth = 0;
   if (kv.cu_q) b = kv::owner(t, kv.batch, [&](int i) { return kv.cu_q[i]; }, &nth);
   const kv::Seq s = kv::seq_of(kv, b);
+  // rows behind the last sequence stay as they are
+  const bool owned = !TREE || (t >= s.lo && t < s.hi);
   // the splits that hold keys of this row
   const int see_hi = TREE ? s.len : max(s.len - s.hi + t + 1, 0);
   const int see_lo = p.window > 0 ? max((TREE ? s.len - (s.hi - s.lo) : see_hi) - p.window, 0) : 0;
   const int s0 = min(see_lo / p.chunk, p.splits - 1);
-  const int s1 = row_ok && see_hi > 0 ? min((see_hi - 1) / p.chunk, p.splits - 1) + 1 : s0;
+  const int s1 = row_ok && owned && see_hi > 0 ? min((see_hi - 1) / p.chunk, p.splits - 1) + 1 : s0;
 
   const float2* ml = p.part_ml + row * p.splits;
   const float* part = p.part_o + row * p.splits * kv.dim;
@@ -383,7 +385,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   sh_sum[wave][lane] = sum;
   sh_l[wave][lane] = l;
   __syncthreads();
-  if (!row_ok || lane >= per || (WPR > 1 && wave > 0)) return;
+  if (!row_ok || !owned || lane >= per || (WPR > 1 && wave > 0)) return;
   float4 all = {0, 0, 0, 0};
   float l_all = 0.0f;
   for (int w = 0; w < WPR; ++w)

@@ -48,9 +48,9 @@ __global__ __launch_bounds__(kThreads) void tree_mask_kernel(TreeMaskParams p) {
   if (p.tree.cu_q)
     b = kv::owner(token, p.tree.batch, [&](int i) { return p.tree.cu_q[i]; }, &unused);
   const Nodes s = nodes_of(p.tree, b);
+  if (token < s.lo || token >= s.lo + s.n) return;    // behind the last sequence
   uint32_t* row = p.mask + long(token) * p.mask_ld;
   for (int w = 0; w < p.words; ++w) row[w] = 0;
-  if (token < s.lo || token >= s.lo + s.n) return;    // an improper cu_q
   int node = token - s.lo, depth = 0, w = node >> 5;
   uint32_t bits = 0;
   for (;;) {

@@ -202,7 +202,7 @@ extern "C" w4a8_status w4a8_kv_keep(const w4a8_kv_view* view, const int32_t* pat
   if (max_path < 1 || path_ld < max_path) return W4A8_ERR_INVALID_ARGUMENT;
   if (view->batch == 0 || view->total_q == 0) return W4A8_OK;
   if (!path_dev || !count_dev) return W4A8_ERR_INVALID_ARGUMENT;
-  if (2l * view->batch * view->kv_heads > kIntMax - 4) return W4A8_ERR_UNSUPPORTED;
+  if (2l * view->batch * view->kv_heads > 4 * kMaxWgs256) return W4A8_ERR_UNSUPPORTED;
   p.path = path_dev;
   p.path_ld = path_ld;
   p.max_path = max_path;
