@@ -126,9 +126,13 @@ __global__ __launch_bounds__(kThreads, DP * R > 128 ? 2 : 3) void tree_attn_kern
   const int first = range.lo / kStep;
   const int last = (range.hi + kStep - 1) / kStep;
 
-  // a lane's row of tile j: drafted token and query head
+  // a lane's row of tile j: drafted token and query head.  Worked out again
+  // wherever it is needed (the asm hides that it is the same): kept, it would take
+  // registers through the whole loop.
   auto row_of = [&](int j, int* t, int* q_head) {
-    const int row = nth * kRows + 16 * j + r16;
+    int first_row = nth * kRows;
+    asm volatile("" : "+s"(first_row));
+    const int row = first_row + 16 * j + r16;
     const int r = min(row, rows - 1);
     *t = r / p.group;
     *q_head = head * p.group + r - *t * p.group;
@@ -216,8 +220,8 @@ __global__ __launch_bounds__(kThreads, DP * R > 128 ? 2 : 3) void tree_attn_kern
           kreg[u][c] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, k_off + 16 * c, slot, 0);
       }
       const uint16_t* sc = kv.scale + at * kv.scale_stride + head;
-      sk_bits[u] = sc[0];
-      sv_bits[u] = sc[kv.kv_heads];
+      sk_bits[u] = __builtin_amdgcn_readfirstlane(sc[0]);
+      sv_bits[u] = __builtin_amdgcn_readfirstlane(sc[kv.kv_heads]);
     }
   };
   auto load_v = [&](int st) {
@@ -264,8 +268,10 @@ __global__ __launch_bounds__(kThreads, DP * R > 128 ? 2 : 3) void tree_attn_kern
     fetch_pages(st + kWaves);
   }
   for (; st < last; st += kWaves) {
-    // scores
+    // scores; the queries are read from LDS here, in every step
     f32x4 acc[R][2];
+    int q_lane = lane;
+    asm volatile("" : "+v"(q_lane));
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -276,9 +282,10 @@ __global__ __launch_bounds__(kThreads, DP * R > 128 ? 2 : 3) void tree_attn_kern
           const f32x4 zero = {0, 0, 0, 0};
           half8_t qf;
           if constexpr (kHeld) qf = q[j][i];
-          else qf = sh_q[j * kKStep + i][lane];
+          else qf = sh_q[j * kKStep + i][q_lane];
           acc[j][u] = mfma16(a, qf, i ? acc[j][u] : zero);
         }
+        if (R > 1) __builtin_amdgcn_sched_barrier(0);
       }
     // factors of the step's two pages; a scale of 0 as in paged_attn.hip
     float sk[2], lv[2], rv[2];
@@ -296,24 +303,34 @@ __global__ __launch_bounds__(kThreads, DP * R > 128 ? 2 : 3) void tree_attn_kern
     // the next step's keys, now that these are in the products
     if (st + kWaves < last) load_k(st + kWaves);
 
+    // where some key is not seen by some row: scores with their scales here, minus
+    // infinity for those, whatever their page's scale
+    const int key0 = st * kStep;
+    if (!(here[0] && here[1] && key0 + kStep <= min(start, range.hi) && key0 >= see_most)) {
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        int t, q_head;
+        const bool row_ok = row_of(j, &t, &q_head);
+        const uint32_t bits = mask_window(p.mask + long(s.lo + t) * p.mask_ld, p.mask_words, key0 - start) >> 4 * quarter;
+        const int key4 = key0 + 4 * quarter;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = key4 + 16 * u + i;
+            const bool seen = row_ok && here[u] && (bits >> (16 * u + i) & 1) && key >= see_lo[j] && key < range.hi;
+            acc[j][u][i] = seen ? __builtin_fmaf(acc[j][u][i], sk[u], lv[u]) : -__builtin_inff();
+          }
+      }
+      sk[0] = sk[1] = 1.0f;
+      lv[0] = lv[1] = 0.0f;
+    }
+
     // weights of the rows: relative to the maximum they have, which moves only
     // when a weight would leave fp16's range
     half8_t pt[R];
-    const int key0 = st * kStep;
-    const bool full = here[0] && here[1] && key0 + kStep <= min(start, range.hi) && key0 >= see_most;
-    auto soften = [&](auto all, int j) {
-      float x[8];
-      if constexpr (!decltype(all)::value) {
-        int t, q_head;
-        const bool row_ok = row_of(j, &t, &q_head);
-        const uint32_t bits = mask_window(p.mask + long(s.lo + t) * p.mask_ld, p.mask_words, key0 - start);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int at = 16 * (i >> 2) + 4 * quarter + (i & 3), key = key0 + at;
-          const bool seen = row_ok && here[i >> 2] && (bits >> at & 1) && key >= see_lo[j] && key < range.hi;
-          x[i] = seen ? __builtin_fmaf(acc[j][i >> 2][i & 3], sk[i >> 2], lv[i >> 2]) : -__builtin_inff();
-        }
-      }
+    for (int j = 0; j < R; ++j) {
       float sum[2];
       auto weights = [&](auto again) {
 #pragma unroll
@@ -322,11 +339,9 @@ __global__ __launch_bounds__(kThreads, DP * R > 128 ? 2 : 3) void tree_attn_kern
           const float c = lv[u] - m[j];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float y;
-            if constexpr (!decltype(all)::value) y = x[4 * u + i] - m[j];
             // again: as the maximum was found, from the rounded score
-            else if constexpr (decltype(again)::value) y = __builtin_fmaf(acc[j][u][i], sk[u], lv[u]) - m[j];
-            else y = __builtin_fmaf(acc[j][u][i], sk[u], c);
+            const float y = decltype(again)::value ? __builtin_fmaf(acc[j][u][i], sk[u], lv[u]) - m[j]
+                                                   : __builtin_fmaf(acc[j][u][i], sk[u], c);
             const float e = __builtin_amdgcn_exp2f(y);
             sum[u] += e;
             pt[j][4 * u + i] = static_cast<_Float16>(e);
@@ -337,10 +352,7 @@ __global__ __launch_bounds__(kThreads, DP * R > 128 ? 2 : 3) void tree_attn_kern
       if (__ballot(!(sum[0] + sum[1] <= kMost))) {
         float mx = -__builtin_inff();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if constexpr (!decltype(all)::value) mx = fmaxf(mx, x[i]);
-          else mx = fmaxf(mx, __builtin_fmaf(acc[j][i >> 2][i & 3], sk[i >> 2], lv[i >> 2]));
-        }
+        for (int i = 0; i < 8; ++i) mx = fmaxf(mx, __builtin_fmaf(acc[j][i >> 2][i & 3], sk[i >> 2], lv[i >> 2]));
         const float m_new = fmaxf(m[j], lifted(row_max(mx)));
         const float alpha = __builtin_amdgcn_exp2f(m[j] - m_new);
         m[j] = m_new;
@@ -352,13 +364,7 @@ __global__ __launch_bounds__(kThreads, DP * R > 128 ? 2 : 3) void tree_attn_kern
       // a sum of 0 (nothing seen) stays 0 whatever the page's scale holds
 #pragma unroll
       for (int u = 0; u < 2; ++u) l[j] += sum[u] == 0.0f ? 0.0f : sum[u] * rv[u];
-    };
-    if (full) {
-#pragma unroll
-      for (int j = 0; j < R; ++j) soften(std::true_type(), j);
-    } else {
-#pragma unroll
-      for (int j = 0; j < R; ++j) soften(std::false_type(), j);
+      if (R > 1) __builtin_amdgcn_sched_barrier(0);
     }
     // whatever the codes of a page with scale 0 are, its values are 0
     if (zero[0] || zero[1]) {
@@ -384,6 +390,7 @@ __global__ __launch_bounds__(kThreads, DP * R > 128 ? 2 : 3) void tree_attn_kern
         }
 #pragma unroll
         for (int j = 0; j < R; ++j) o[j][4 * c + col] = mfma16(a, pt[j], o[j][4 * c + col]);
+        if (R > 1) __builtin_amdgcn_sched_barrier(0);
       }
     }
     if (st + kWaves < last) {
