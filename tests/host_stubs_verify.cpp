@@ -38,16 +38,18 @@ hipError_t launch_tree_mask(const TreeMaskParams& p, hipStream_t) {
   need(p.tree.parents && p.tree.total_q > 0 && p.mask && p.words >= 1 && p.mask_ld >= p.words);
   return hipErrorNoDevice;
 }
-hipError_t launch_tree_attn(const AttnParams& p, int tiles, hipStream_t) {
+hipError_t launch_tree_attn(const TreeAttnParams& p, hipStream_t) {
   check(p.kv);
-  need(p.mask && p.mask_words >= 1 && p.mask_ld >= p.mask_words);
-  need(tiles == 1 || tiles == 2 || (tiles == 4 && p.kv.dim <= 128));
-  need(p.splits >= 1 && p.splits <= 256 && p.chunk > 0 && p.chunk % 64 == 0);
-  need(attn_tiles(p.kv, p.group, 16 * tiles) * p.kv.kv_heads * p.splits <= kMaxWgs256);
-  need(p.group * p.kv.kv_heads == p.q_heads && (p.splits == 1 || p.part_ml));
+  need(p.mask && p.mask_words >= 1 && p.mask_ld >= p.mask_words && (p.tiles == 1 || p.tiles == 2));
+  need(p.group * p.kv.kv_heads == p.q_heads && (p.group == 1 || p.group_inverse > 0));
+  const long tiles = attn_tiles(p.kv, p.group, 16 * p.tiles);
+  need(p.groups >= tiles && long(p.groups) * p.kv.kv_heads <= kMaxWgs256);
+  need(p.shares == 0 || (p.shares == p.groups && p.kv.batch <= kTreeBatch && p.least > 0 && p.part_ml && p.part_o));
+  // work in its units, of the longest sequences the table holds, fits what a lane counts
+  const long longest = (long(p.kv.max_pages) << p.kv.page_shift) / kTreeStep + 1;
+  need(p.unit >= 0 && p.unit <= 26 && tiles * ((longest >> p.unit) + 1) <= kMostWork);
   return hipErrorNoDevice;
 }
-hipError_t launch_attn_join(const AttnParams&, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_tree_accept(const AcceptParams& p, hipStream_t) {
   check(p.tree);
   need(p.path && p.max_path >= 1 && p.path_ld >= p.max_path && p.count && p.tokens && p.new_lens);

@@ -140,6 +140,47 @@ def test_one_node_each_without_cu_q():
     assert (o[0] == 0).all()
 
 
+@pytest.mark.parametrize("count,nodes,dim", [(65, 3, 64), (130, 20, 16), (300, 1, 32), (5000, 1, 16), (4500, 2, 16)])
+def test_many_sequences(count, nodes, dim):
+    """More sequences than lanes, some of them long (so that their tiles are split
+    where that is done at all), some without nodes."""
+    dev = device()
+    log(f"tree attention {count} sequences of up to {nodes}")
+    rng = np.random.default_rng(21)
+    spans = [(int(n) + int(rng.integers(0, 40)), int(n)) for n in rng.integers(0, nodes + 1, count)]
+    spans[count // 2] = (3000, nodes)
+    spans[-1] = (2000, nodes)
+    batch = Batch(spans, 64, 1, dim, 22)
+    _, see = trees(batch)
+    q = batch.rng.standard_normal((batch.tokens, 2, dim)).astype(np.float16)
+    for most in (None, 100):
+        check(batch, q, see, attend(batch, q, mask_of(see, 1), dev, max_q=nodes, max_len=most))
+
+
+def test_tables_that_are_improper():
+    """cu_q that does not ascend or ends beyond the rows, lengths and pages out of
+    range: nothing outside the buffers is touched (results mean nothing), and what
+    the other sequences get is untouched memory or finite."""
+    import torch
+    dev = device()
+    log("tree attention improper tables")
+    batch = Batch([(100, 20), (40, 10), (64, 10)], 16, 2, 64, 23)
+    q = batch.rng.standard_normal((40, 4, 64)).astype(np.float16)
+    mask = np.full((40, 1), -1, np.int32)
+    for cu in ([0, 40, 10, 40], [5, 2, 1, 0], [0, 100, 200, 300], [-7, 40, 40, 90], [2 ** 31 - 1] * 4, [-2 ** 31] * 4):
+        for lens in ([100, 40, 64], [-5, 2 ** 31 - 1, 10], [0, 0, 0]):
+            st = batch.device(dev)
+            st["cu_q"], st["seq_lens"] = put(np.array(cu, np.int32), dev), put(np.array(lens, np.int32), dev)
+            guard = torch.full((42, 4, 64), 7.0, dtype=torch.float16, device=dev)
+            attend(batch, q, mask, dev, state=st, out=guard[1:41])
+            w4.tree_mask(put(np.zeros(40, np.int32), dev), st["seq_lens"], cu_q=st["cu_q"])
+            path, count, _, _ = w4.tree_accept(put(np.zeros(40, np.int32), dev), put(np.zeros(40, np.int32), dev),
+                                               put(np.zeros(40, np.int32), dev), st["seq_lens"], cu_q=st["cu_q"])
+            w4.kv_keep(st["cache"], st["scale"], st["block_table"], st["seq_lens"], path, count, cu_q=st["cu_q"])
+            torch.cuda.synchronize()
+            assert (guard[0] == 7).all() and (guard[41] == 7).all()
+
+
 def test_values_that_are_not_ordinary():
     """NaN in a query stays in its rows; a row that sees nothing is 0 all the
     same; scales of pages that are not seen do not reach a row; absent pages are

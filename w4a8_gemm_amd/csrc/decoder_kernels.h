@@ -113,11 +113,6 @@ struct AttnParams {
   int chunk;                  // and the keys of each (a multiple of 64; the last takes the rest)
   float2* part_ml;            // splits > 1: maximum and sum of [token][query head][split],
   float* part_o;              // and its unnormalised values, [dim] each
-  // drafted trees (null elsewhere): bit j of a new token's row says whether it
-  // sees the sequence's new token j; all positions before those are seen
-  const uint32_t* mask = nullptr;
-  long mask_ld = 0;
-  int mask_words = 0;
 };
 
 // Row tiles of the attention: the rows of a sequence and kv head are its
@@ -131,9 +126,6 @@ constexpr int kAttnRows = 16;   // rows of a tile (paged_attn.hip)
 hipError_t launch_paged_attn(const AttnParams& p, hipStream_t stream);
 // 32 rows a wave, 4 waves, or 8 where 64 < dim <= 128 (paged_attn_tile.hip)
 hipError_t launch_paged_attn_tile(const AttnParams& p, int waves, hipStream_t stream);
-// drafted trees: 16 * tiles rows a workgroup, tiles 1, 2 or, with dim <= 128, 4
-// (tree_attn.hip)
-hipError_t launch_tree_attn(const AttnParams& p, int tiles, hipStream_t stream);
 hipError_t launch_attn_join(const AttnParams& p, hipStream_t stream);
 
 // Turns a HIP status into the C ABI's and keeps it for

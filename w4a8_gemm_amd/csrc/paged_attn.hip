@@ -335,8 +335,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void attn_split_kernel
 
 // The splits of a row, joined in a fixed order of sums.  WPR waves share a
 // row; each takes 64 / (dim / 4) splits at a time, dim / 4 lanes a split.
-// TREE: the rows of a sequence see parts of all splits that hold keys of it.
-template <int WPR, bool TREE>
+template <int WPR>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   const KvArgs& kv = p.kv;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -347,13 +346,11 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   int b = t, nth = 0;
   if (kv.cu_q) b = kv::owner(t, kv.batch, [&](int i) { return kv.cu_q[i]; }, &nth);
   const kv::Seq s = kv::seq_of(kv, b);
-  // rows behind the last sequence stay as they are
-  const bool owned = !TREE || (t >= s.lo && t < s.hi);
   // the splits that hold keys of this row
-  const int see_hi = TREE ? s.len : max(s.len - s.hi + t + 1, 0);
-  const int see_lo = p.window > 0 ? max((TREE ? s.len - (s.hi - s.lo) : see_hi) - p.window, 0) : 0;
+  const int see_hi = max(s.len - s.hi + t + 1, 0);
+  const int see_lo = p.window > 0 ? max(see_hi - p.window, 0) : 0;
   const int s0 = min(see_lo / p.chunk, p.splits - 1);
-  const int s1 = row_ok && owned && see_hi > 0 ? min((see_hi - 1) / p.chunk, p.splits - 1) + 1 : s0;
+  const int s1 = row_ok && see_hi > 0 ? min((see_hi - 1) / p.chunk, p.splits - 1) + 1 : s0;
 
   const float2* ml = p.part_ml + row * p.splits;
   const float* part = p.part_o + row * p.splits * kv.dim;
@@ -385,7 +382,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   sh_sum[wave][lane] = sum;
   sh_l[wave][lane] = l;
   __syncthreads();
-  if (!row_ok || !owned || lane >= per || (WPR > 1 && wave > 0)) return;
+  if (!row_ok || lane >= per || (WPR > 1 && wave > 0)) return;
   float4 all = {0, 0, 0, 0};
   float l_all = 0.0f;
   for (int w = 0; w < WPR; ++w)
@@ -427,13 +424,8 @@ hipError_t launch_attn_join(const AttnParams& p, hipStream_t stream) {
   // few rows: four waves read a row's splits together
   const long rows = long(p.kv.total_q) * p.q_heads;
   const bool few = rows <= kJoinFewRows;
-  const void* fn;
-  if (p.mask)
-    fn = few ? reinterpret_cast<const void*>(&attn_join_kernel<4, true>)
-             : reinterpret_cast<const void*>(&attn_join_kernel<1, true>);
-  else
-    fn = few ? reinterpret_cast<const void*>(&attn_join_kernel<4, false>)
-             : reinterpret_cast<const void*>(&attn_join_kernel<1, false>);
+  const void* fn = few ? reinterpret_cast<const void*>(&attn_join_kernel<4>)
+                       : reinterpret_cast<const void*>(&attn_join_kernel<1>);
   return hipLaunchKernel(fn, dim3(unsigned(few ? rows : (rows + 3) / 4)), dim3(256), args, 0, stream);
 }
 

@@ -18,36 +18,45 @@ namespace {
 constexpr long kIntMax = 2147483647l;
 
 // What tree_attention launches for a batch: row tiles of 16 a workgroup, and the
-// split of the keys.
+// workgroups that share each kv head's work.
 struct TreePlan {
-  int tiles;
-  int splits, chunk;
-  long wgs;
+  int tiles, groups, shares, least, unit;
   size_t ml_bytes, workspace;
 };
 
-constexpr long kComputeUnits = 256;
-constexpr int kMaxSplits = 256;
+constexpr long kResident = 512;          // workgroups: two a compute unit
+constexpr int kLeastSteps = 16;
+constexpr long kMuchWork = 65536;
 
 TreePlan plan_tree(const KvArgs& kv, int q_heads, int max_q, int max_len) {
   TreePlan pl;
   const int group = q_heads / kv.kv_heads;
   const long rows = long(kv.cu_q ? max_q : 1) * group;
-  pl.tiles = rows <= 16 ? 1 : rows <= 32 || kv.dim > 128 ? 2 : 4;
-  const long units = attn_tiles(kv, group, 16 * pl.tiles) * kv.kv_heads;
-  const long rows_all = long(kv.total_q) * q_heads;
-  const long least = 256;
-  const double keys = double(units) * max_len;
-  double want = std::max(keys / double(4 * kComputeUnits), double(max_len) / kMaxSplits);
-  if (rows_all > kMaxWgs256) want = max_len;
-  const long chunk = std::max(1l, (long(want) + least) / least) * least;
-  const long splits = std::max(1l, (max_len + chunk - 1) / chunk);
-  pl.splits = int(splits);
-  pl.chunk = int(std::min(chunk, 1l << 30));
-  pl.wgs = units * splits;
-  const size_t parts = splits > 1 ? size_t(rows_all) * size_t(splits) : 0;
-  pl.ml_bytes = (parts * 8 + 255) / 256 * 256;
-  pl.workspace = parts > 0 ? pl.ml_bytes + parts * size_t(kv.dim) * 4 : 0;
+  const long steps = (long(max_len) + kTreeStep - 1) / kTreeStep;
+  // 32 rows a workgroup share the conversion of the codes, 16 leave more
+  // workgroups and less to do before and after the keys.  By the products of 16
+  // rows and a step there are: 3500 (one tree of 26 tokens over 2001 keys, heads
+  // 32 / 8) 13.8 us with 16 rows and 16.4 with 32; 43000 (6 of up to 200 over 1700)
+  // 20 and 24; 164000 (16 of up to 64 over 4096) 89 and 73, (4 of 13 over 50000) 86
+  // and 75.  64 rows take too many registers for more than two waves a SIMD and
+  // measured 27, 33, 82 and 72.
+  const long products = attn_tiles(kv, group, 16) * kv.kv_heads * steps;
+  pl.tiles = rows <= 16 || products < kMuchWork ? 1 : 2;
+  // Tiles are split where they do not fill the device and there are keys for
+  // two parts of kLeastSteps (one tree over 2001 keys: parts of 8 steps 16.9 us, of
+  // 16 13.8).  Three workgroups a unit measured 77 against 73 us on the 16 trees,
+  // 75 and 75 on the long ones.
+  const long tiles = attn_tiles(kv, group, 16 * pl.tiles);
+  pl.least = kLeastSteps;
+  pl.shares = int(std::max(kResident / kv.kv_heads, tiles));
+  if (steps < 2 * kLeastSteps || kResident / kv.kv_heads <= tiles || kv.batch > kTreeBatch) pl.shares = 0;
+  pl.groups = int(pl.shares ? long(pl.shares) : tiles);
+  const long longest = (long(kv.max_pages) << kv.page_shift) / kTreeStep + 1;
+  for (pl.unit = 0; tiles * ((longest >> pl.unit) + 1) > kMostWork && pl.unit < 26; ++pl.unit) {
+  }
+  const size_t parts = pl.shares ? size_t(pl.groups) * kv.kv_heads * 16 * pl.tiles : 0;
+  pl.ml_bytes = parts * 8;
+  pl.workspace = pl.ml_bytes + parts * size_t(kv.dim) * 4;
   return pl;
 }
 
@@ -130,7 +139,7 @@ extern "C" w4a8_status w4a8_tree_attention(const uint16_t* q_dev, int ldq, int q
                                            int mask_ld, int mask_words, int max_q, int max_len,
                                            float scale, int window, uint16_t* out_dev, int ldo,
                                            void* workspace_dev, size_t workspace_bytes, void* stream) {
-  AttnParams p;
+  TreeAttnParams p;
   w4a8_status st = check_view(view, &p.kv);
   if (st != W4A8_OK) return st;
   if (max_q < 0 || max_len < 0 || window < 0 || !std::isfinite(scale) || mask_words < 1 ||
@@ -143,7 +152,7 @@ extern "C" w4a8_status w4a8_tree_attention(const uint16_t* q_dev, int ldq, int q
   if (!mask_dev || !rows_ok(q_dev, ldq, cols) || !rows_ok(out_dev, ldo, cols))
     return W4A8_ERR_INVALID_ARGUMENT;
   const TreePlan pl = plan_tree(p.kv, q_heads, max_q, max_len);
-  if (pl.wgs > kMaxWgs256) return W4A8_ERR_UNSUPPORTED;
+  if (long(pl.groups) * p.kv.kv_heads > kMaxWgs256) return W4A8_ERR_UNSUPPORTED;
   if (pl.workspace > 0) {
     if (workspace_bytes < pl.workspace) return W4A8_ERR_BUFFER_TOO_SMALL;
     if (!workspace_dev || !aligned16(workspace_dev)) return W4A8_ERR_INVALID_ARGUMENT;
@@ -156,17 +165,18 @@ extern "C" w4a8_status w4a8_tree_attention(const uint16_t* q_dev, int ldq, int q
   p.group = q_heads / p.kv.kv_heads;
   p.scale_log2e = scale * 1.44269504f;
   p.window = window;
-  p.splits = pl.splits;
-  p.chunk = pl.chunk;
+  p.tiles = pl.tiles;
+  p.groups = pl.groups;
+  p.shares = pl.shares;
+  p.least = pl.least;
+  p.unit = pl.unit;
   p.part_ml = static_cast<float2*>(workspace_dev);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace_dev) + (pl.workspace ? pl.ml_bytes : 0));
   p.mask = mask_dev;
   p.mask_ld = mask_ld;
   p.mask_words = mask_words;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  st = device_status(launch_tree_attn(p, pl.tiles, s));
-  if (st != W4A8_OK || pl.splits == 1) return st;
-  return device_status(launch_attn_join(p, s));
+  p.group_inverse = p.group > 1 ? uint32_t(((1ull << 32) + p.group - 1) / p.group) : 0u;
+  return device_status(launch_tree_attn(p, static_cast<hipStream_t>(stream)));
 }
 
 extern "C" w4a8_status w4a8_tree_accept(const int32_t* drafted_dev, const int32_t* parents_dev,

@@ -30,6 +30,31 @@ struct TreeMaskParams {
 };
 hipError_t launch_tree_mask(const TreeMaskParams& p, hipStream_t stream);
 
+struct TreeAttnParams {
+  KvArgs kv;
+  const uint16_t* q;
+  uint16_t* out;
+  int ldq, ldo;
+  int q_heads, group;         // group = q_heads / kv_heads
+  uint32_t group_inverse;     // 2^32 / group, rounded up (group > 1)
+  float scale_log2e;          // score scale * log2(e)
+  int window;                 // 0: none
+  const uint32_t* mask;       // bit j of a new token's row: it sees the sequence's new token j
+  long mask_ld;
+  int mask_words;
+  int tiles;                  // rows of a workgroup, in tiles of 16: 1 or 2
+  int groups;                 // workgroups of a kv head: for all row tiles, and for
+  int shares;                 // about as many parts as this of all work; 0: tiles are not split
+  int least;                  // steps of a part, at least
+  int unit;                   // log2 of the steps in which work is counted
+  float2* part_ml;            // split tiles: [groups][kv_heads][16 * tiles] maximum and sum of the
+  float* part_o;              // rows of a workgroup's part, and their unnormalised values, [dim] each
+};
+constexpr int kTreeStep = 32;          // keys of a step
+constexpr int kTreeBatch = 4096;       // most sequences whose tiles are split: 64 a lane
+constexpr long kMostWork = (1l << 25) - 1;   // what a lane counts: 64 of them fit an int
+hipError_t launch_tree_attn(const TreeAttnParams& p, hipStream_t stream);
+
 struct AcceptParams {
   TreeBatch tree;
   const int32_t* drafted;
