@@ -588,9 +588,12 @@ w4a8_status w4a8_kv_keep(const w4a8_kv_view* view, const int32_t* path_dev, int 
  *                or infinite, or a setting on the device is not valid
  *   probs_dev    [rows] fp32, may be NULL: the drawn token's share of the kept
  *                weights; 0 or NaN in the cases of -1
+ *   workspace_dev  16-byte aligned, w4a8_sample_workspace_size bytes (may be NULL
+ *                when that is 0); no initialisation, calls in flight at once need
+ *                one each
  * rows == 0 is a no-op.  Errors: INVALID_ARGUMENT (null pointer, ld < vocab,
  * rows > W4A8_M_MAX, temperature negative or not finite, a NaN setting),
- * UNSUPPORTED (vocab > W4A8_VOCAB_MAX), DEVICE. */
+ * UNSUPPORTED (vocab > W4A8_VOCAB_MAX), BUFFER_TOO_SMALL, DEVICE. */
 #define W4A8_VOCAB_MAX (1 << 19)
 typedef struct {
   float temperature;
@@ -602,9 +605,10 @@ typedef struct {
   const float* top_p_dev;
   const float* min_p_dev;
 } w4a8_sampling;
+size_t w4a8_sample_workspace_size(int logits_f32, int rows, int vocab);
 w4a8_status w4a8_sample(const void* logits_dev, int logits_f32, int ld, int rows, int vocab,
                         const float* u_dev, const w4a8_sampling* settings, int32_t* tokens_dev,
-                        float* probs_dev, void* stream);
+                        float* probs_dev, void* workspace_dev, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------ pages of the cache
  * Which page holds what, on the device: block tables as in w4a8_kv_view, and

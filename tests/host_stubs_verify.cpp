@@ -66,6 +66,19 @@ hipError_t launch_kv_keep(const KeepParams& p, hipStream_t) {
 hipError_t launch_sample(const SampleParams& p, hipStream_t) {
   need(p.logits && p.u && p.tokens && p.rows > 0 && p.rows <= (1 << 22) && p.vocab >= 1);
   need(p.vocab <= W4A8_VOCAB_MAX && p.ld >= p.vocab);
+  if (p.maxima) {
+    const long each = p.f32 ? 4 : 8, chunks = (p.vocab + each - 1 + each - 1) / each;   // the most a row has
+    need(p.tops && p.masses && long(p.rows) * p.blocks <= kMaxWgs256);
+    need(long(p.blocks) * kSampleSpan >= chunks && long(p.groups) * kSampleGroup >= chunks && p.parts * 64l >= chunks);
+    // the parts of the workspace, one behind the other
+    auto at = [&](const void* q) { return reinterpret_cast<const char*>(q) - reinterpret_cast<const char*>(p.tops); };
+    const long rows = p.rows, list = at(p.list);
+    need(at(p.masses) >= rows * p.blocks * 8 && list - at(p.masses) >= rows * p.parts * 8 + rows * kSampleBins * 8);
+    need(!p.bins || (at(p.bins) - at(p.masses) >= rows * p.parts * 8 && list - at(p.bins) >= rows * kSampleBins * 8));
+    need(at(p.maxima) - list >= rows * kSampleList * 8 && at(p.listed) - at(p.maxima) >= rows * p.groups * 4);
+    need(size_t(at(p.listed) + rows * 4) <= w4a8_sample_workspace_size(p.f32, p.rows, p.vocab));
+    need(p.sums || !p.bins);
+  }
   return hipErrorNoDevice;
 }
 hipError_t launch_kv_fork(const ForkParams& p, hipStream_t) {

@@ -32,7 +32,8 @@ def main():
     L.w4a8_tree_attention.argtypes = [P, I, I, P, P, I, I, I, I, F, I, P, I, P, Z, P]
     L.w4a8_tree_accept.argtypes = [P, P, P, P, P, I, I, P, I, I, P, P, P, P]
     L.w4a8_kv_keep.argtypes = [P, P, I, I, P, P]
-    L.w4a8_sample.argtypes = [P, I, I, I, I, P, P, P, P, P]
+    L.w4a8_sample_workspace_size.argtypes, L.w4a8_sample_workspace_size.restype = [I, I, I], Z
+    L.w4a8_sample.argtypes = [P, I, I, I, I, P, P, P, P, P, Z, P]
     L.w4a8_kv_fork.argtypes = [P, I, I, P, I, P, I, I, P, I, P, I, P, P, P]
     L.w4a8_kv_alloc_workspace_size.argtypes, L.w4a8_kv_alloc_workspace_size.restype = [I, I], Z
     L.w4a8_kv_alloc.argtypes = [P, I, I, P, I, P, I, I, P, I, P, I, P, P, P, P, P, P, Z, P]
@@ -77,14 +78,15 @@ def main():
         size = some(page)
         a_need = L.w4a8_kv_alloc_workspace_size(b, n) if rng.random() < 0.9 else 16
         c_need = L.w4a8_kv_compact_workspace_size(n) if rng.random() < 0.9 else 0
+        f32, vocab = pick([0, 1]), some(pick([1, 50257, 1 << 19]))
+        s_need = L.w4a8_sample_workspace_size(f32, b, vocab) if rng.random() < 0.9 else 64
         out = {
             "mask": L.w4a8_tree_mask(at(), at(), at(cu), b, t, at(), ld, words, at(), None),
             "attention": L.w4a8_tree_attention(at(), some(4096 * 256), q_heads, vp, at(), ld, words, max_q, max_len,
                                                pick(floats), pick([0, 0, 5, -1]), at(), some(4096 * 256), at(), ws, None),
             "accept": L.w4a8_tree_accept(at(), at(), at(), at(), at(cu), b, t, at(), ld, words, at(), at(), at(), None),
             "keep": L.w4a8_kv_keep(vp, at(), ld, words, at(), None),
-            "sample": L.w4a8_sample(at(), pick([0, 1]), some(1 << 19), b, some(pick([1, 50257, 1 << 19])), at(), sp, at(),
-                                    at(), None),
+            "sample": L.w4a8_sample(at(), f32, some(1 << 19), b, vocab, at(), sp, at(), at(), at(), s_need, None),
             "fork": L.w4a8_kv_fork(at(), some(2000), width, at(), b, at(), n, size, at(), some(pick([0, 5, 1 << 20])),
                                    at(12288), some(2000), at(12288), at(12288), None),
             "alloc": L.w4a8_kv_alloc(at(), some(2000), width, at(), b, at(), n, size, at(), some(3), at(12288), some(2000),

@@ -163,6 +163,38 @@ def test_settings_of_each_row():
     check(x, u, *run(x, u, dev, **filters), **filters)
 
 
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+@pytest.mark.parametrize("vocab", [8191, 8192, 20000, 70001])
+def test_long_rows_of_every_kind(vocab, dtype):
+    """Rows that are looked at by several workgroups before: flat ones, whose kept
+    tokens are too many to list, steep ones, ties across the bound, few finite
+    logits, none, a NaN at an end; with every kind of filter."""
+    dev = device()
+    log(f"sample long rows {vocab} {dtype.__name__}")
+    rng = np.random.default_rng(vocab)
+    x = logits(12, vocab, rng, dtype)
+    x[0] = (0.01 * rng.standard_normal(vocab)).astype(dtype)
+    x[1] = (30 * rng.standard_normal(vocab)).astype(dtype)
+    x[2] = rng.integers(0, 3, vocab)
+    x[3] = 1.0
+    x[4] = -np.inf
+    x[4, vocab - 3:] = [1.0, 2.0, 1.5]
+    x[5] = -np.inf
+    x[6, vocab - 1] = np.nan
+    x[7, 0] = np.inf
+    x[8, ::2] = -np.inf
+    x[9] = np.sort(x[9])
+    x[10] = np.sort(x[10])[::-1]
+    u = rng.random(12).astype(np.float32)
+    for filters in FILTERS + [dict(top_k=600), dict(top_k=513, top_p=0.3), dict(top_k=vocab - 1), dict(min_p=1e-4),
+                              dict(min_p=0.5, top_p=0.999), dict(min_p=1.0), dict(top_p=0.5, temperature=20.0),
+                              dict(min_p=1e-30, temperature=0.3), dict(top_k=40, min_p=0.2)]:
+        check(x, u, *run(x, u, dev, **filters), **filters)
+    each = dict(top_k=rng.choice([0, 5, 700], 12).astype(np.int32), top_p=rng.choice([0.7, 1.0], 12).astype(np.float32),
+                temperature=rng.choice([0.0, 1.0], 12).astype(np.float32), min_p=rng.choice([0.0, 0.1], 12).astype(np.float32))
+    check(x, u, *run(x, u, dev, **each), **each)
+
+
 def test_the_whole_range_of_u():
     """Every token of a small row is drawn over its share of [0, 1)."""
     dev = device()

@@ -75,11 +75,12 @@ def test_accept_and_keep_arguments():
 
 
 def test_sample_arguments():
-    def call(x=FAKE, f32=0, ld=100, rows=3, vocab=100, u=FAKE, s=(1.0, 0, 1.0, 0.0), tokens=FAKE, probs=None, dev=None):
+    def call(x=FAKE, f32=0, ld=100, rows=3, vocab=100, u=FAKE, s=(1.0, 0, 1.0, 0.0), tokens=FAKE, probs=None, dev=None,
+             ws=None, ws_bytes=0):
         s = w4.Sampling(*s)
         for name in dev or ():
             setattr(s, name + "_dev", FAKE)
-        return w4.lib.w4a8_sample(x, f32, ld, rows, vocab, u, ctypes.byref(s), tokens, probs, None)
+        return w4.lib.w4a8_sample(x, f32, ld, rows, vocab, u, ctypes.byref(s), tokens, probs, ws, ws_bytes, None)
     nan, inf = float("nan"), float("inf")
     statuses(call, [(dict(x=None), 1), (dict(x=FAKE + 1), 1), (dict(x=FAKE + 2, f32=1), 1), (dict(ld=99), 1),
                     (dict(rows=-1), 1), (dict(rows=(1 << 22) + 1), 1), (dict(vocab=0), 1), (dict(u=None), 1),
@@ -87,7 +88,13 @@ def test_sample_arguments():
                     (dict(s=(inf, 0, 1.0, 0.0)), 1), (dict(s=(1.0, 0, nan, 0.0)), 1), (dict(s=(1.0, 0, 1.0, nan)), 1),
                     (dict(vocab=(1 << 19) + 1, ld=1 << 20), 2), (dict(rows=0, x=None), 0),
                     (dict(s=(nan, 0, 1.0, 0.0), dev=("temperature",), rows=0), 0)])
-    assert w4.lib.w4a8_sample(FAKE, 0, 100, 3, 100, FAKE, None, FAKE, None, None) == 1
+    assert w4.lib.w4a8_sample(FAKE, 0, 100, 3, 100, FAKE, None, FAKE, None, None, 0, None) == 1
+    need = w4.lib.w4a8_sample_workspace_size(0, 3, 50000)
+    assert need > 0 and w4.lib.w4a8_sample_workspace_size(0, 3, 100) == 0
+    assert w4.lib.w4a8_sample_workspace_size(0, 3, 1 << 20) == 0 and w4.lib.w4a8_sample_workspace_size(0, -3, 50000) == 0
+    long = dict(vocab=50000, ld=50000)
+    statuses(call, [(long, 3), (dict(**long, ws=FAKE, ws_bytes=need - 1), 3), (dict(**long, ws_bytes=need), 1),
+                    (dict(**long, ws=FAKE + 8, ws_bytes=need), 1)])
 
 
 def test_page_arguments():
@@ -137,7 +144,7 @@ def tensors(device="cuda:0"):
     i32 = lambda *shape: torch.empty(shape, dtype=torch.int32, device=device)
     f32 = lambda *shape: torch.empty(shape, dtype=torch.float32, device=device)
     t.nodes, t.cu, t.mask, t.path, t.count, t.refs, t.u = i32(3), i32(4), i32(3, 1), i32(3, 2), i32(3), i32(9), f32(5)
-    t.cos_sin = f32(40, 64)
+    t.cos_sin, t.five = f32(40, 64), i32(5)
     return t
 
 
@@ -148,8 +155,9 @@ CALLS = {
     "tree_attention": (lambda t, **kw: w4.tree_attention(t.q, *t.kv, t.mask, **kw), 2, 1),
     "tree_accept": (lambda t, **kw: w4.tree_accept(t.nodes, t.nodes, t.nodes, t.kv[3], **kw), 4, 4),
     "kv_keep": (lambda t, **kw: w4.kv_keep(*t.kv, t.path, t.count, **kw), 0, 0),
-    "sample": (lambda t, **kw: w4.sample(t.a, t.u, **kw), 2, 2),
-    "sample, settings": (lambda t, **kw: w4.sample(t.a.float(), t.u, t.u, top_p=t.u, probs=t.u, **kw), 1, 1),
+    "sample": (lambda t, **kw: w4.sample(t.a, t.u, **kw), 3, 2),
+    "sample, settings": (lambda t, **kw: w4.sample(t.a.float(), t.u, t.u, top_p=t.u, probs=t.u, **kw), 2, 1),
+    "sample, given": (lambda t, **kw: w4.sample(t.a, t.u, tokens=t.five, probs=t.u, workspace=t.blob, **kw), 0, 0),
     "kv_fork": (lambda t, **kw: w4.kv_fork(t.kv[2], t.kv[3], t.refs, t.nodes, 16, **kw), 3, 3),
     "kv_alloc": (lambda t, **kw: w4.kv_alloc(t.kv[2], t.kv[3], t.refs, 1, 16, **kw), 7, 6),
     "kv_compact": (lambda t, **kw: w4.kv_compact(t.kv[2], t.refs, **kw), 7, 6),
@@ -215,7 +223,7 @@ def test_tensors_that_do_not_fit_are_refused(devices_seen):
                 lambda: w4.sample(here.a, here.u, there.u), lambda: w4.sample(here.a, here.u, top_k=here.u),
                 lambda: w4.sample(here.a, here.u, top_p=here.u[:2]), lambda: w4.sample(here.a, here.u, tokens=here.nodes),
                 lambda: w4.sample(here.a, here.u, probs=there.u), lambda: w4.sample(here.a.t(), here.u),
-                lambda: w4.sample(here.a.double(), here.u),
+                lambda: w4.sample(here.a.double(), here.u), lambda: w4.sample(here.a, here.u, workspace=there.blob),
                 lambda: w4.kv_fork(here.kv[2], there.kv[3], here.refs, here.nodes, 16),
                 lambda: w4.kv_fork(here.kv[2], here.kv[3], there.refs, here.nodes, 16),
                 lambda: w4.kv_fork(here.kv[2], here.kv[3], here.refs, there.nodes, 16),
@@ -280,4 +288,4 @@ def test_abi_under_asan_and_ubsan(tmp_path):
     for name, status in seen.items():
         assert 1 in status and 7 in status, (name, status)       # refused, and reached a launch
     assert all(2 in seen[name] for name in ("attention", "keep", "sample", "fork", "alloc", "compact", "copy"))
-    assert all(3 in seen[name] for name in ("attention", "alloc", "compact"))
+    assert all(3 in seen[name] for name in ("attention", "sample", "alloc", "compact"))

@@ -122,7 +122,8 @@ def _load():
         "w4a8_tree_attention": (I, [P, I, I, P, P, I, I, I, I, ctypes.c_float, I, P, I, P, Z, P]),
         "w4a8_tree_accept": (I, [P, P, P, P, P, I, I, P, I, I, P, P, P, P]),
         "w4a8_kv_keep": (I, [P, P, I, I, P, P]),
-        "w4a8_sample": (I, [P, I, I, I, I, P, P, P, P, P]),
+        "w4a8_sample_workspace_size": (Z, [I, I, I]),
+        "w4a8_sample": (I, [P, I, I, I, I, P, P, P, P, P, Z, P]),
         "w4a8_kv_fork": (I, [P, I, I, P, I, P, I, I, P, I, P, I, P, P, P]),
         "w4a8_kv_alloc_workspace_size": (Z, [I, I]),
         "w4a8_kv_alloc": (I, [P, I, I, P, I, P, I, I, P, I, P, I, P, P, P, P, P, P, Z, P]),
@@ -808,7 +809,8 @@ def kv_keep(cache, scale, block_table, seq_lens, path, count, cu_q=None, stream=
 
 
 @_on_device
-def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, probs=None, stream=None):
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, probs=None, workspace=None,
+           stream=None):
     """A token for each row of logits [rows, vocab] (float16 or float32) from the
     random numbers u, float32 [rows] in [0, 1): returns (tokens int32 [rows], probs
     float32 [rows], the share of the kept weights that each token has).  Settings
@@ -837,8 +839,16 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=Non
         probs = _empty((rows,), torch.float32, logits.device, stream)
     else:
         _vector("probs", probs, torch.float32, dev, rows)
-    _check(lib.w4a8_sample(logits.data_ptr(), int(f32), _ld(logits), rows, vocab, u.data_ptr(), ctypes.byref(s),
-                           tokens.data_ptr(), probs.data_ptr(), _stream_of(logits, stream)), "w4a8_sample")
+    ld = _ld(logits)
+    need = lib.w4a8_sample_workspace_size(int(f32), rows, vocab)
+    if need and workspace is None:
+        workspace = _empty(need, torch.uint8, logits.device, stream, returned=False)
+    elif workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace: expected a contiguous CUDA tensor on device {dev}")
+    _check(lib.w4a8_sample(logits.data_ptr(), int(f32), ld, rows, vocab, u.data_ptr(), ctypes.byref(s),
+                           tokens.data_ptr(), probs.data_ptr(), _ptr(workspace),
+                           workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                           _stream_of(logits, stream)), "w4a8_sample")
     return tokens, probs
 
 

@@ -76,6 +76,9 @@ w4a8_status check_tree(const int32_t* parents, const int32_t* lens, const int32_
   return W4A8_OK;
 }
 
+// Rows from which on sampling looks at them in several workgroups before.
+constexpr int kLongRow = 8192;
+
 // log2 of a page size, or -1
 int page_shift_of(int page_size) {
   for (int shift = 4; shift <= 10; ++shift)
@@ -220,9 +223,46 @@ extern "C" w4a8_status w4a8_kv_keep(const w4a8_kv_view* view, const int32_t* pat
   return device_status(launch_kv_keep(p, static_cast<hipStream_t>(stream)));
 }
 
+namespace {
+
+// Whether a call asks its rows before it draws, and the workspace for it.
+struct SamplePlan {
+  int blocks, groups, parts;
+  size_t masses_at, bins_at, list_at, maxima_at, listed_at, workspace;      // tops first
+};
+
+SamplePlan plan_sample(int logits_f32, int rows, int vocab) {
+  SamplePlan pl = {};
+  if (vocab < kLongRow) return pl;
+  const int each = logits_f32 ? 4 : 8;
+  const long chunks = (long(vocab) + each - 2) / each + 1;      // wherever the row begins
+  pl.blocks = int((chunks + kSampleSpan - 1) / kSampleSpan);
+  pl.groups = int((chunks + kSampleGroup - 1) / kSampleGroup);
+  pl.parts = int((chunks + 63) / 64);
+  if (long(rows) * pl.blocks > kMaxWgs256) return SamplePlan{};
+  pl.masses_at = size_t(rows) * pl.blocks * 8;
+  pl.bins_at = pl.masses_at + size_t(rows) * pl.parts * 8;
+  pl.list_at = pl.bins_at + size_t(rows) * kSampleBins * 8;
+  pl.maxima_at = pl.list_at + size_t(rows) * kSampleList * 8;
+  pl.listed_at = pl.maxima_at + size_t(rows) * pl.groups * 4;
+  pl.workspace = pl.listed_at + size_t(rows) * 4;
+  return pl;
+}
+
+bool sample_sizes_ok(int rows, int vocab) {
+  return rows >= 0 && rows <= W4A8_M_MAX && vocab >= 1 && vocab <= W4A8_VOCAB_MAX;
+}
+
+}  // namespace
+
+extern "C" size_t w4a8_sample_workspace_size(int logits_f32, int rows, int vocab) {
+  return sample_sizes_ok(rows, vocab) ? plan_sample(logits_f32, rows, vocab).workspace : 0;
+}
+
 extern "C" w4a8_status w4a8_sample(const void* logits_dev, int logits_f32, int ld, int rows, int vocab,
                                    const float* u_dev, const w4a8_sampling* settings,
-                                   int32_t* tokens_dev, float* probs_dev, void* stream) {
+                                   int32_t* tokens_dev, float* probs_dev, void* workspace_dev,
+                                   size_t workspace_bytes, void* stream) {
   if (rows < 0 || rows > W4A8_M_MAX || vocab < 1 || ld < vocab || !settings)
     return W4A8_ERR_INVALID_ARGUMENT;
   if (vocab > W4A8_VOCAB_MAX) return W4A8_ERR_UNSUPPORTED;
@@ -233,6 +273,9 @@ extern "C" w4a8_status w4a8_sample(const void* logits_dev, int logits_f32, int l
   if (rows == 0) return W4A8_OK;
   if (!logits_dev || !u_dev || !tokens_dev) return W4A8_ERR_INVALID_ARGUMENT;
   if (reinterpret_cast<uintptr_t>(logits_dev) % (logits_f32 ? 4 : 2)) return W4A8_ERR_INVALID_ARGUMENT;
+  const SamplePlan pl = plan_sample(logits_f32, rows, vocab);
+  if (workspace_bytes < pl.workspace) return W4A8_ERR_BUFFER_TOO_SMALL;
+  if (pl.workspace > 0 && (!workspace_dev || !aligned16(workspace_dev))) return W4A8_ERR_INVALID_ARGUMENT;
   SampleParams p;
   p.logits = logits_dev;
   p.f32 = logits_f32;
@@ -243,6 +286,22 @@ extern "C" w4a8_status w4a8_sample(const void* logits_dev, int logits_f32, int l
   p.s = s;
   p.tokens = tokens_dev;
   p.probs = probs_dev;
+  p.blocks = pl.blocks;
+  p.groups = pl.groups;
+  p.parts = pl.parts;
+  // no row's weights are all wanted if every row has a top_k, or only a min_p
+  const bool counts = !s.top_k_dev && s.top_k > 0 && s.top_k < vocab;
+  const bool only_least = !s.top_p_dev && s.top_p >= 1.0f && !s.min_p_dev && s.min_p > 0.0f;
+  const bool greedy = !s.temperature_dev && s.temperature == 0.0f;
+  p.sums = !counts && !only_least && !greedy;
+  const bool shares = p.sums && (s.top_p_dev || s.top_p < 1.0f);
+  char* const ws = static_cast<char*>(workspace_dev);
+  p.tops = pl.workspace ? reinterpret_cast<uint64_t*>(ws) : nullptr;
+  p.masses = pl.workspace ? reinterpret_cast<uint64_t*>(ws + pl.masses_at) : nullptr;
+  p.bins = pl.workspace && shares ? reinterpret_cast<uint64_t*>(ws + pl.bins_at) : nullptr;
+  p.list = pl.workspace ? reinterpret_cast<uint2*>(ws + pl.list_at) : nullptr;
+  p.maxima = pl.workspace ? reinterpret_cast<uint32_t*>(ws + pl.maxima_at) : nullptr;
+  p.listed = pl.workspace ? reinterpret_cast<int32_t*>(ws + pl.listed_at) : nullptr;
   return device_status(launch_sample(p, static_cast<hipStream_t>(stream)));
 }
 

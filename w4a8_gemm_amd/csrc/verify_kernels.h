@@ -86,7 +86,19 @@ struct SampleParams {
   w4a8_sampling s;
   int32_t* tokens;
   float* probs;               // may be null
+  // long rows: what is known of them before (workspace; null: nothing)
+  int blocks, groups, parts;  // of a row: workgroups, groups of chunks, stretches of 64 chunks
+  bool sums;                  // some row may need sums of all its weights
+  uint32_t* maxima;           // [rows][groups] largest keys
+  uint64_t* tops;             // [rows][blocks] largest key, and bit 32: a logit is NaN or infinite
+  uint64_t* masses;           // [rows][parts] sums of weights
+  uint64_t* bins;             // [rows][kSampleBins] sums of weights; null: no row may need them
+  uint2* list;                // [rows][kSampleList] tokens of one bin: key, place
+  int32_t* listed;            // [rows] their number; more than kSampleList: not listed
 };
+constexpr int kSampleBins = 2048, kSampleList = 4096;
+constexpr int kSampleSpan = 2048;       // chunks of 16 bytes that a workgroup looks at before
+constexpr int kSampleGroup = 8;         // chunks of a group
 hipError_t launch_sample(const SampleParams& p, hipStream_t stream);
 
 // The pages of a pool, their reference counts and the tables that name them.
