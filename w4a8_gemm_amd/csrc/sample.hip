@@ -71,6 +71,7 @@ struct Logit<uint16_t> {
     return b & 0x8000u ? ~b & 0xFFFFu : b | 0x8000u;
   }
   static __device__ __forceinline__ uint32_t key_of(float v) { return key(f2h_bits(v)); }
+  static __device__ __forceinline__ double of_bits(uint32_t b) { return double(h2f(uint16_t(b))); }
   static __device__ __forceinline__ double value(uint32_t key) {
     return double(h2f(uint16_t(key & 0x8000u ? key ^ 0x8000u : ~key)));
   }
@@ -85,6 +86,7 @@ struct Logit<uint32_t> {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
   }
   static __device__ __forceinline__ uint32_t key_of(float v) { return key(__builtin_bit_cast(uint32_t, v)); }
+  static __device__ __forceinline__ double of_bits(uint32_t b) { return double(__builtin_bit_cast(float, b)); }
   static __device__ __forceinline__ double value(uint32_t key) {
     return double(__builtin_bit_cast(float, key & 0x80000000u ? key ^ 0x80000000u : ~key));
   }
@@ -145,21 +147,31 @@ struct Shared {
   int fews;
 };
 
-__device__ __forceinline__ uint64_t shfl_up64(uint64_t x, int d) {
-  const uint32_t lo = __shfl_up(uint32_t(x), d), hi = __shfl_up(uint32_t(x >> 32), d);
+// Sums of the lanes up to each: within rows of 16, then the rows before.
+template <int CONTROL, int ROWS>
+__device__ __forceinline__ uint64_t lanes_before(uint64_t x) {
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, uint32_t(x), CONTROL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, uint32_t(x >> 32), CONTROL, ROWS, 0xF, false);
   return lo | uint64_t(hi) << 32;
+}
+__device__ __forceinline__ uint64_t wave_upto(uint64_t x) {
+  x += lanes_before<0x111, 0xF>(x);              // from 1, 2, 4, 8 lanes below
+  x += lanes_before<0x112, 0xF>(x);
+  x += lanes_before<0x114, 0xF>(x);
+  x += lanes_before<0x118, 0xF>(x);
+  x += lanes_before<0x142, 0xA>(x);              // row 0's last to row 1, 2's to 3
+  return x + lanes_before<0x143, 0xC>(x);        // the first half's to the second
+}
+__device__ __forceinline__ uint64_t last_lane(uint64_t x) {
+  return uint32_t(__builtin_amdgcn_readlane(uint32_t(x), 63)) |
+         uint64_t(uint32_t(__builtin_amdgcn_readlane(uint32_t(x >> 32), 63))) << 32;
 }
 
 // Sums of the threads before this one; *total that of all.  All threads call it.
 template <int THREADS = kThreads, typename S>
 __device__ __forceinline__ uint64_t block_before(S& sh, uint64_t x, uint64_t* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint64_t upto = x;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t y = shfl_up64(upto, d);
-    if (lane >= d) upto += y;
-  }
+  const uint64_t upto = wave_upto(x);
   __syncthreads();                        // the last call's sums have been read
   if (lane == 63) sh.sums[wave] = upto;
   __syncthreads();
@@ -255,23 +267,23 @@ struct Weigh {
       : largest(Logit<T>::value(top)), turn(1.4426950408889634 / double(temperature)) {}
   // log2 of the weight
   __device__ __forceinline__ double log2_of(uint32_t key) const { return (Logit<T>::value(key) - largest) * turn; }
+  __device__ __forceinline__ double log2_of_bits(uint32_t bits) const { return (Logit<T>::of_bits(bits) - largest) * turn; }
   __device__ __forceinline__ double operator()(uint32_t key) const { return of_log2(log2_of(key)); }
+  // 2^(t + 44): adding 1.5 * 2^52 rounds t to a whole number, which stands in the
+  // sum's low bits and is added to the exponent of 2^(the rest)
   static __device__ __forceinline__ double of_log2(double t) {
-    if (!(t > -64.0)) return 0.0;
-    const double whole = __builtin_rint(t);
-    return __builtin_ldexp(exp2_near0(t - whole), int(whole) + kUnitBits);
+    const double sum = t + 0x1.8p52;
+    const int whole = int(__builtin_bit_cast(uint64_t, sum));
+    const uint64_t w = __builtin_bit_cast(uint64_t, exp2_near0(t - (sum - 0x1.8p52)));
+    const double y = __builtin_bit_cast(double, w + (uint64_t(uint32_t(whole + kUnitBits) << 20) << 32));
+    return t > -64.0 ? y : 0.0;
   }
 };
 __device__ __forceinline__ uint64_t units(double w) {
   return __builtin_bit_cast(uint64_t, w + 0x1p52) & ((1ull << 52) - 1);
 }
 
-__device__ __forceinline__ uint64_t wave_sum64(uint64_t x) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1)
-    x += uint64_t(uint32_t(__shfl_xor(uint32_t(x), d))) | uint64_t(uint32_t(__shfl_xor(uint32_t(x >> 32), d))) << 32;
-  return x;
-}
+__device__ __forceinline__ uint64_t wave_sum64(uint64_t x) { return last_lane(wave_upto(x)); }
 
 // What long rows are asked before: workgroups of 256 threads take kSpan chunks.
 constexpr int kAheadThreads = 256;
@@ -375,9 +387,9 @@ __global__ __launch_bounds__(kAheadThreads) void sample_sum_kernel(SampleParams 
     uint64_t mass = 0;
 #pragma unroll
     for (int e = 0; e < L::kEach; ++e) {
-      const uint32_t key = L::key(bits_of<T>(mine, e));
-      const double t = weight.log2_of(key);
-      const uint64_t x = key > L::kLowest ? units(weight.of_log2(t)) : 0;
+      // minus infinity, also where there is no logit, weighs 0
+      const double t = weight.log2_of_bits(bits_of<T>(mine, e));
+      const uint64_t x = units(weight.of_log2(t));
       if (bins) {
         if (x) atomicAdd(&sums[bin_of(t)], static_cast<unsigned long long>(x));
       } else {
@@ -430,15 +442,15 @@ __global__ __launch_bounds__(kAheadThreads) void sample_split_kernel(SampleParam
     uint64_t mass = 0;
 #pragma unroll
     for (int e = 0; e < L::kEach; ++e) {
-      const uint32_t key = L::key(bits_of<T>(mine, e));
-      const double t = weight.log2_of(key);
-      const int in = key > L::kLowest && t > -64.0 ? bin_of(t) : kSampleBins;
+      const uint32_t bits = bits_of<T>(mine, e);
+      const double t = weight.log2_of_bits(bits);
+      const int in = t > -64.0 ? bin_of(t) : kSampleBins;
       if (in < bin) {
         const double x = weight.of_log2(t);
         if (x >= least) mass += units(x);
       } else if (in == bin) {
         const int at = atomicAdd(&sh.listed, 1);
-        if (at < kSpan) sh.list[at] = make_uint2(key, c * L::kEach + e);
+        if (at < kSpan) sh.list[at] = make_uint2(L::key(bits), c * L::kEach + e);
       }
     }
     mass = wave_sum64(mass);
@@ -548,6 +560,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
 
   const Weigh<T> weight(top, s.temperature);
   const double least = least_of(s);
+  const float u = u_raw >= 0.0f ? fminf(u_raw, 0x1.fffffep-1f) : 0.0f;
+  auto target_of = [&](uint64_t all) { return uint64_t(double(u) * double(all)) + 1; };
 
   // The tokens kept: keys above `border`, and the first `ties` that have it.  Once
   // they are known to lie among few, these are in sh.list.
@@ -635,6 +649,11 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
       target -= before;
       prefix = prefix << width | uint32_t(n - 1 - at);
       shift = low;
+      // of maxima only a bound is wanted
+      if (kMaxima && shift <= 10) {
+        *key_out = max(prefix << shift, L::kLowest + 1);
+        return true;
+      }
       // what is kept has at least these leading bits
       if (!kMaxima && !listed && shift > 0) {
         __syncthreads();
@@ -647,6 +666,51 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
     *left = target;
     return true;
   };
+  // Draws from the listed tokens, all there are that may be kept, a thread each: a
+  // token's place in the order of falling logits, and the weights before it there
+  // and in the order of numbers, are worked out by looking at all.
+  auto from_few = [&](int most) {
+    const int n = sh.listed;
+    uint2 own = {0, 0};
+    uint64_t mass = 0;
+    double w = 0.0;
+    if (tid < n) {
+      own = sh.list[tid];
+      w = weight(own.x);
+      mass = units(w);
+      sh.few[tid] = make_uint4(uint32_t(mass), uint32_t(mass >> 32), own.y, own.x);
+    }
+    __syncthreads();
+    int rank = 0;
+    uint64_t before = 0;
+    if (tid < n) {
+      for (int i = 0; i < n; ++i) {
+        const uint4 x = sh.few[i];
+        const bool first = x.w > own.x || (x.w == own.x && x.z < own.y);
+        rank += first;
+        before += first ? x.x | uint64_t(x.y) << 32 : 0;
+      }
+      if (rank == min(most, n) - 1) sh.found_before = before + mass;      // of all that count
+    }
+    __syncthreads();
+    if (tid < n) {
+      const bool kept = rank < most && (s.top_p >= 1.0f || before < share_of(s, sh.found_before)) && w >= least;
+      if (!kept) mass = 0;
+      sh.few[tid].x = uint32_t(mass);
+      sh.few[tid].y = uint32_t(mass >> 32);
+    }
+    __syncthreads();
+    if (tid >= n || mass == 0) return;
+    uint64_t upto = 0, all = 0;
+    for (int i = 0; i < n; ++i) {
+      const uint4 x = sh.few[i];
+      const uint64_t m = x.x | uint64_t(x.y) << 32;
+      all += m;
+      upto += x.z <= own.y ? m : 0;
+    }
+    const uint64_t target = target_of(all);
+    if (upto >= target && upto - mass < target) finish(int(own.y), float(w / double(all)));
+  };
   // The n-th largest of the maxima is not above the n-th largest of all logits.
   const bool by_count = s.top_k > 0, by_mass = s.top_p < 1.0f;
   uint32_t at_key;
@@ -654,11 +718,19 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
   if (by_count && s.top_k <= kThreads / 2) {
     if (select(std::false_type(), std::true_type(), [&](uint64_t) { return uint64_t(s.top_k); }, &at_key, &left))
       gather(at_key);
+    if (listed && sh.listed <= kFew) {
+      from_few(s.top_k);
+      return;
+    }
   } else if (ahead && !by_count && !by_mass && least > 0.0) {
     // only min_p: a logit that is certainly not above the least one kept
     const double down = log(double(fminf(s.min_p, 1.0f))) * double(s.temperature);
     const double from = weight.largest + down - 1e-12 * (fabs(weight.largest) - down);
     gather(max(L::key_of(float(from)) - 1, L::kLowest + 1));
+    if (listed && sh.listed <= kFew) {
+      from_few(kFew);
+      return;
+    }
   }
   if (by_count &&
       select(std::false_type(), std::false_type(), [&](uint64_t) { return uint64_t(s.top_k); }, &at_key, &left)) {
@@ -689,8 +761,6 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
   const double border_weight = weight(border);
   const uint64_t border_units = units(border_weight);
   if (border == L::kLowest || border_weight < least) ties = 0;
-  const float u = u_raw >= 0.0f ? fminf(u_raw, 0x1.fffffep-1f) : 0.0f;
-  auto target_of = [&](uint64_t all) { return uint64_t(double(u) * double(all)) + 1; };
   auto kept = [&](uint32_t key, double* w) -> uint64_t {
     if (key <= border) return 0;
     *w = weight(key);
@@ -762,8 +832,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
       same += key == border && border != L::kLowest;
     }
     mass = wave_sum64(mass);
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) same += __shfl_xor(same, d);
+    same = uint32_t(wave_sum64(same));
     const int part = c >> 6;
     if (lane == 0 && part < parts) {
       sh.mass[part] = mass;
@@ -801,13 +870,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
     key[e] = L::key(bits_of<T>(w, e));
     same += key[e] == border && border != L::kLowest;
   }
-  uint32_t rank = same;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t y = __shfl_up(rank, d);
-    if (lane >= d) rank += y;
-  }
-  rank += sh.count[part] - same;                // equal tokens before this lane's
+  uint32_t rank = uint32_t(wave_upto(same)) + sh.count[part] - same;    // equal tokens before this lane's
   uint64_t mass[kEach], own = 0;
   double exact[kEach];
 #pragma unroll
@@ -820,12 +883,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
     }
     own += mass[e];
   }
-  uint64_t upto = own;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t y = shfl_up64(upto, d);
-    if (lane >= d) upto += y;
-  }
+  const uint64_t upto = wave_upto(own);
   uint64_t at = upto - own;
   if (at < target && target <= upto) {
     bool done = false;
