@@ -35,7 +35,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBinBits = 11;
 constexpr int kBins = 1 << kBinBits;
@@ -144,7 +144,7 @@ struct Shared {
   uint2 list[kList];          // (key, place) of the tokens that may be kept, in no order
   int listed;                 // their number; more than kList: not listed
   uint4 few[kFew];            // (weight's two words, place, key) of kept tokens
-  int fews;
+  int fews, hits;
 };
 
 // Sums of the lanes up to each: within rows of 16, then the rows before.
@@ -511,7 +511,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
   uint32_t top = wave_max_u32(mine);
   const bool wave_bad = __ballot(bad) != 0;
   if (lane == 0) sh.sums[wave] = top | uint64_t(wave_bad) << 32;
-  if (tid == 0) sh.listed = sh.fews = 0;
+  if (tid == 0) sh.listed = sh.fews = sh.hits = 0;
   __syncthreads();
   bad = false;
 #pragma unroll
@@ -586,9 +586,18 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
       }
     };
     if (ahead) {
-      for (int g = tid / kGroup; g < p.groups; g += kThreads / kGroup) {
+      // the groups that have such tokens first: each has at least one
+      int* const hits = reinterpret_cast<int*>(sh.mass);
+      for (int g = tid; g < p.groups; g += kThreads) {
         if (maxima[g] < from) continue;
-        const int c = g * kGroup + tid % kGroup;
+        const int at = atomicAdd(&sh.hits, 1);
+        if (at < kList) hits[at] = g;
+      }
+      __syncthreads();
+      const int n = sh.hits;
+      if (n > kList) return;                     // listed stays false
+      for (int i = tid / kGroup; i < n; i += kThreads / kGroup) {
+        const int c = hits[i] * kGroup + tid % kGroup;
         const uint4 v = row.load(c);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         look(c, w);
@@ -657,7 +666,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
       // what is kept has at least these leading bits
       if (!kMaxima && !listed && shift > 0) {
         __syncthreads();
-        if (tid == 0) sh.listed = 0;
+        if (tid == 0) sh.listed = sh.hits = 0;
         __syncthreads();
         gather(max(prefix << shift, ties ? border : border + 1));
       }
@@ -715,7 +724,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
   const bool by_count = s.top_k > 0, by_mass = s.top_p < 1.0f;
   uint32_t at_key;
   uint64_t left;
-  if (by_count && s.top_k <= kThreads / 2) {
+  if (by_count && s.top_k <= (ahead ? kList : kThreads) / 2) {
     if (select(std::false_type(), std::true_type(), [&](uint64_t) { return uint64_t(s.top_k); }, &at_key, &left))
       gather(at_key);
     if (listed && sh.listed <= kFew) {
@@ -806,12 +815,12 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
   // at the border
   const int parts = (row.chunks + 63) / 64;
   __syncthreads();
-  if (split || (ahead && sums_all(s))) {
+  if (listed || (ahead && sums_all(s))) {
     for (int i = tid; i < parts; i += kThreads) {
-      sh.mass[i] = p.masses[r * p.parts + i];
+      sh.mass[i] = listed && !split ? 0 : p.masses[r * p.parts + i];
       sh.count[i] = 0;
     }
-    if (split) {
+    if (listed) {
       __syncthreads();
       each_listed([&](uint32_t key, uint32_t place) {
         const uint32_t part = place / kEach >> 6;
