@@ -81,6 +81,10 @@ class DecoderLayer:
     def new_cache(self, batch: Batch, device):
         self.cache, self.scale = w4.kv_cache(batch.pages, self.kv_heads, self.head_dim, batch.page, device)
 
+    def attend(self, q, k, v, cos_sin, where, batch: Batch):
+        q = w4.rope_append(q, k, v, cos_sin, *where, cu_q=batch.cu_q)
+        return w4.paged_attention(q, *where, cu_q=batch.cu_q, max_q=batch.max_q, max_len=batch.max_len)
+
     def __call__(self, x, residual, cos_sin, batch: Batch):
         """x is what the layer before adds to the residual stream (or the
         embeddings, residual None); returns the same pair for the next."""
@@ -88,9 +92,7 @@ class DecoderLayer:
         h, a8, s_a = w4.rms_norm_quant(x, self.norm_in, residual=residual)
         qkv = self.qkv.from_int8(a8, s_a).view(x.shape[0], -1, self.head_dim)
         q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], dim=1)
-        q = w4.rope_append(q, k, v, cos_sin, *where, cu_q=batch.cu_q)
-        o = w4.paged_attention(q, *where, cu_q=batch.cu_q, max_q=batch.max_q, max_len=batch.max_len)
-        y = self.o(o.view(x.shape[0], -1))
+        y = self.o(self.attend(q, k, v, cos_sin, where, batch).view(x.shape[0], -1))
         h, a8, s_a = w4.rms_norm_quant(y, self.norm_mlp, residual=h)
         a8, s_a = w4.silu_mul_quant(self.gate_up.from_int8(a8, s_a))
         return self.down.from_int8(a8, s_a), h
