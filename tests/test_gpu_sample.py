@@ -164,7 +164,7 @@ def test_settings_of_each_row():
 
 
 @pytest.mark.parametrize("dtype", [np.float16, np.float32])
-@pytest.mark.parametrize("vocab", [8191, 8192, 20000, 70001])
+@pytest.mark.parametrize("vocab", [8191, 8192, 20000, 32767, 32768, 70001])
 def test_long_rows_of_every_kind(vocab, dtype):
     """Rows that are looked at by several workgroups before: flat ones, whose kept
     tokens are too many to list, steep ones, ties across the bound, few finite

@@ -21,6 +21,15 @@
 //                        top_p in 2048 bins of 1/32 of log2 weight
 //   sample_split_kernel  for top_p, the bin in which its share is reached: weights
 //                        above it by stretches, and the bin's tokens as a list
+//
+// Reading bounds sample_max_kernel (244 MB 48 us, 5 TB/s).  Where all weights count,
+// their powers of two in 64 bits bound sample_sum_kernel and sample_split_kernel,
+// about 30 instructions a logit; in bins, also the additions in LDS.  sample_kernel
+// is latency: two dozen barriers, 7 to 14 us, and two rows a compute unit.
+// Measured, graph replays of the whole call: one row of 32000 fp16 logits with top_k
+// and top_p 16.5 us (21 in one kernel); 64 of 128256 with top_p 50 (max
+// 7, sums 17, split 15, drawing 13); 801 of 152064, settings of each row's own, 211
+// (48, 47, 44, 71); 33 of 50257 fp32 with min_p 10.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -35,6 +44,9 @@ namespace {
 
 using namespace dev;
 
+// Two workgroups of 512 fit a compute unit, one of 1024.  1024 measured, us: 801 rows of
+// 152064 with top_k 50 134 against 109, with top_p 341 and 314, one row with top_k 50
+// 23.7 and 26.5 (19.6 since groups are found first).
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBinBits = 11;
@@ -133,7 +145,10 @@ __device__ __forceinline__ uint32_t bits_of(const uint32_t (&w)[4], int e) {
 }
 
 constexpr int kList = kSampleList;
-constexpr int kFew = 256;                // tokens that are drawn from without another look at the row
+// Up to so many listed tokens are ranked by looking at all for each, n^2 / 64 steps of
+// a wave: 256 take about 10 us, what a selection among more and the sums of
+// stretches take.
+constexpr int kFew = 256;
 
 struct Shared {
   uint64_t mass[kParts];      // of bins, then of stretches

@@ -6,7 +6,10 @@
 // parent outside [0, child) means none.  Node 0 is the root: the sequence's last
 // certain token, whose sampled successor selects among its children.
 //
-// All three are latency: a launch and loads that wait for each other.
+// All three are latency: a launch and loads that wait for each other.  Measured,
+// graph replays of tree_accept and kv_keep: one tree of 26 nodes, heads 32 / 8 of
+// 128, 6.5 us (2.9 and 4.3 in the kernels); 96 of up to 64 nodes 10.7 (5.7 and 7.1),
+// where the 1.9 MB that are read and written would take 0.4.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
