@@ -18,7 +18,7 @@
 // other, and code that runs once and has to be fetched, about a nanosecond a byte.
 // Measured, graph replays with the join: 16 trees of up to 64 tokens over up to
 // 4096 keys, heads 32 / 8 of 128, 73 us = 0.32 PFLOP/s; 4 of up to 13 over 50000
-// 75 us = 3.2 TB/s; 6 of up to 200 over 1700 under a window of 1024, heads 16 / 4
+// 71 us = 3.4 TB/s; 6 of up to 200 over 1700 under a window of 1024, heads 16 / 4
 // of 64, 20 us; one of 26 over 2001 13.8 us.
 
 #include <hip/hip_runtime.h>
@@ -639,8 +639,10 @@ __global__ __launch_bounds__(256) void tree_join_kernel(TreeAttnParams p) {
   const int per = kv.dim >> 2;                      // lanes of a row
   const int groups = 256 / per;
   const int lane = threadIdx.x % per, group = threadIdx.x / per;
-  // few parts: a row belongs to one group; else all groups share a row's parts
-  const bool shared = parts > 4;
+  // few parts: a row belongs to one group; else all groups share a row's parts,
+  // with two barriers a row.  Up to 4, 8, 16 and 32 parts measured, us: 4 trees of 13
+  // tokens over 50000 keys 75, 73, 71 and 71; 3 of them 71, 72, 69 and 68.
+  const bool shared = parts > 16;
   __shared__ float4 sh_o[256];
   __shared__ float2 sh_ml[256];
   const int stride = (parts - 1) * (shared ? 1 : groups);
