@@ -273,3 +273,53 @@ def test_captured_and_on_two_streams():
         torch.cuda.synchronize()
         for got, want in zip(outs, alone):
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_more_groups_than_a_list_holds():
+    """Rows of which every 128 bytes hold a token at the bound, and others whose
+    few tokens above it are far apart; counts around the largest that maxima bound."""
+    dev = device()
+    log("sample many groups")
+    rng = np.random.default_rng(10)
+    vocab = 1 << 19
+    for dtype in (np.float16, np.float32):
+        x = np.zeros((4, vocab), dtype)
+        x[1] = rng.integers(0, 2, vocab)
+        x[2] = logits(1, vocab, rng, dtype)[0]
+        x[3, ::4099] = 8.0
+        u = np.array([0.3, 0.999, 0.6, 0.1], np.float32)
+        for filters in (dict(top_k=50), dict(top_k=2048), dict(top_k=2049, top_p=0.9), dict(min_p=0.4),
+                        dict(top_k=100, top_p=0.5, temperature=0.3)):
+            check(x, u, *run(x, u, dev, **filters), **filters)
+
+
+def test_long_rows_with_settings_of_each():
+    """As for short rows: settings of every row, and at the ends of their ranges."""
+    dev = device()
+    log("sample long rows, settings per row")
+    rng = np.random.default_rng(12)
+    rows, vocab = 70, 30001
+    x, u = logits(rows, vocab, rng, np.float16), rng.random(rows).astype(np.float32)
+    u[:5] = 0.0, 1 - 2.0 ** -24, 1.0, -1.0, np.nan
+    filters = dict(temperature=rng.choice([0.0, 0.5, 1.0, 1.7, 1e-30, 1e30], rows).astype(np.float32),
+                   top_k=rng.choice([0, 0, -1, 1, 40, 300, 2048, 30000, 30001, 2 ** 31 - 1], rows).astype(np.int32),
+                   top_p=rng.choice([0.0, 0.2, 0.9, 1.0, 1 - 2.0 ** -24], rows).astype(np.float32),
+                   min_p=rng.choice([0.0, 0.02, 2.0], rows).astype(np.float32))
+    check(x, u, *run(x, u, dev, **filters), **filters)
+    filters["top_p"][7] = filters["min_p"][8] = filters["temperature"][9] = np.nan
+    tokens, probs = run(x, u, dev, **filters)
+    assert (tokens[7:10] == -1).all() and np.isnan(probs[7:10]).all()
+    assert (np.delete(tokens, [7, 8, 9]) >= 0).all()
+
+
+def test_long_rows_beyond_32_bits():
+    import torch
+    dev = device()
+    log("sample far long rows")
+    far = torch.empty(4 * (1 << 29) + 40960, dtype=torch.float16, device=dev)
+    x = far.as_strided((5, 40000), ((1 << 29), 1))
+    rng = np.random.default_rng(13)
+    host, u = logits(5, 40000, rng, np.float16), rng.random(5).astype(np.float32)
+    x.copy_(put(host, dev))
+    for filters in (dict(top_p=0.9), dict(top_k=100), dict(min_p=0.1), dict()):
+        check(host, u, *run(x, u, dev, **filters), **filters)

@@ -748,7 +748,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
     }
   } else if (ahead && !by_count && !by_mass && least > 0.0) {
     // only min_p: a logit that is certainly not above the least one kept
-    const double down = log(double(fminf(s.min_p, 1.0f))) * double(s.temperature);
+    // (its weight as computed; the largest temperatures round many to 1)
+    const double down = (log(double(fminf(s.min_p, 1.0f))) - 1e-12) * double(s.temperature);
     const double from = weight.largest + down - 1e-12 * (fabs(weight.largest) - down);
     gather(max(L::key_of(float(from)) - 1, L::kLowest + 1));
     if (listed && sh.listed <= kFew) {
