@@ -387,7 +387,10 @@ w4a8_status w4a8_silu_mul_quant(const uint16_t* gate_dev, int ldg,
  * hold, nothing outside the pool and the rows is read or written: lengths are
  * clamped to max_pages * page_size, offsets to total_q, page numbers outside
  * [0, num_pages) count as absent (nothing is written there, its keys are not
- * seen).  Apart from absent pages such contents give unspecified results. */
+ * seen).  Apart from absent pages such contents give unspecified results.
+ * Where a length is past the table's end, w4a8_rope_append and w4a8_kv_keep
+ * write nothing there, and before it what the length says: the earlier tokens
+ * stay as they are. */
 #define W4A8_HEAD_DIM_MAX 256
 #define W4A8_HEADS_MAX 4096
 typedef struct {

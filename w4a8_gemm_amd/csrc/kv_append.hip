@@ -126,17 +126,18 @@ __device__ __forceinline__ void append_block(const AppendParams& p, int unit) {
     b = slot_index;
   }
   const kv::Seq s = kv::seq_of(kv, b);
-  const int n = s.hi - s.lo;
-  const int start = max(s.len - n, 0);                 // position of the first new token
+  const int n = s.hi - s.lo, len = kv::told_length(kv, b);
+  const int start = max(len - n, 0);                   // position of the first new token
   const int page_index = (start >> kv.page_shift) + nth;
+  // every wave of a team takes the same way here and below
+  if (nth < 0 || page_index >= kv.max_pages) return;
   const int page_begin = page_index << kv.page_shift;
   const int begin = max(start, page_begin);            // new positions in this page
-  const int end = min(s.len, page_begin + (1 << kv.page_shift));
-  // every wave of a team takes the same way here
-  if (nth < 0 || begin >= end) return;
+  const int end = min(len, page_begin + (1 << kv.page_shift));
+  if (begin >= end) return;
   const int first = begin - page_begin;                // slots before it hold earlier tokens
   const int count = end - begin;
-  const int token0 = s.hi - (s.len - begin);           // new token at position `begin`
+  const int token0 = s.hi - (len - begin);             // new token at position `begin`
 
   const uint16_t* src = (which ? p.v : p.k) + long(head) * kv.dim;
   const long ld = which ? p.ldv : p.ldk;
@@ -274,7 +275,7 @@ __device__ __forceinline__ void rotate_queries(const AppendParams& p, long index
       int b = int(t), nth = 0;
       if (kv.cu_q) b = kv::owner(int(t), kv.batch, [&](int i) { return kv.cu_q[i]; }, &nth);
       const kv::Seq s = kv::seq_of(kv, b);
-      pos = s.len - s.hi + int(t);
+      pos = kv::told_length(kv, b) - s.hi + int(t);
     }
     turn = turn_of(p, it, pos);
   }

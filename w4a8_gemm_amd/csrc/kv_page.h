@@ -33,6 +33,11 @@ static __device__ __forceinline__ Seq seq_of(const KvArgs& a, int b) {
   return s;
 }
 
+// The length as the caller has it, which may be past the end of the table: what
+// writes places its tokens by it, so that those past the end are not written
+// (page_at has no page for them) and none is moved over the tokens before.
+static __device__ __forceinline__ int told_length(const KvArgs& a, int b) { return max(a.lens[b], 0); }
+
 // The largest b with first(b) <= w, for an ascending first: the sequence that
 // owns virtual index w; *index is w's place in it.
 // first(0) is 0 for a proper cu_q; an improper one gives some sequence in range.

@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kThreads) void kv_keep_kernel(KeepParams p, int uni
   const int which = unit / kv.kv_heads & 1;
   const int b = unit / (2 * kv.kv_heads);
   const kv::Seq s = kv::seq_of(kv, b);
-  const int n = s.hi - s.lo, start = s.len - n;
+  const int n = s.hi - s.lo, start = kv::told_length(kv, b) - n;
   const int count = min(min(p.count[b], p.max_path), n);
   if (count <= 0 || start < 0) return;
   const int32_t* const path = p.path + long(b) * p.path_ld;
@@ -157,7 +157,8 @@ __global__ __launch_bounds__(kThreads) void kv_keep_kernel(KeepParams p, int uni
   };
   auto scale_of = [&](int page) { return uint32_t(kv.scale[page * kv.scale_stride + scale_at]) & 0x7FFFu; };
 
-  for (int index = start >> kv.page_shift; index <= (start + count - 1) >> kv.page_shift; ++index) {
+  const int last = min((start + count - 1) >> kv.page_shift, kv.max_pages - 1);
+  for (int index = start >> kv.page_shift; index <= last; ++index) {
     const int begin = index << kv.page_shift;
     const int i0 = max(begin - start, 0), i1 = min(begin + slot_mask + 1 - start, count);
     const int held = max(start - begin, 0);       // slots with earlier tokens
