@@ -652,7 +652,7 @@ w4a8_status w4a8_kv_fork(const int32_t* block_table_dev, int block_table_ld, int
  *   src_dev, dst_dev  [batch] int32: pairs in the order of sequences, then -1
  *   counts_dev   [2] int32: the number of pairs, and that of entries that got no
  *                page (they are -1: nothing is written there), because none was
- *                free or the table has no room
+ *                free or the table has no room; at most 2^31 - 1
  *   workspace_dev  w4a8_kv_alloc_workspace_size bytes, 16-byte aligned, no
  *                initialisation */
 size_t w4a8_kv_alloc_workspace_size(int batch, int num_pages);

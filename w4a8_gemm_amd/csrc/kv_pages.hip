@@ -36,30 +36,23 @@ __device__ __forceinline__ int length_of(const int32_t* lens, int b, const Table
   return min(max(lens[b], 0), t.max_pages << shift);
 }
 
-// sum over a wave, in every lane
-__device__ __forceinline__ int wave_sum(int x) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
-  return x;
-}
-
 // Sums of the values of the threads before this one; *total that of all.  Every
 // thread of the workgroup calls it.
-template <int THREADS>
-__device__ __forceinline__ int block_before(int x, int* total) {
+template <int THREADS, typename Sum = int>
+__device__ __forceinline__ Sum block_before(Sum x, Sum* total) {
   constexpr int kW = THREADS / 64;
-  __shared__ int sums[kW];
+  __shared__ Sum sums[kW];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int upto = x;
+  Sum upto = x;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(upto, d);
+    const Sum y = __shfl_up(upto, d);
     if (lane >= d) upto += y;
   }
   __syncthreads();                       // the last call's sums have been read
   if (lane == 63) sums[wave] = upto;
   __syncthreads();
-  int before = 0, all = 0;
+  Sum before = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < kW; ++w) {
     if (w < wave) before += sums[w];
@@ -194,7 +187,8 @@ __global__ __launch_bounds__(kScanThreads) void alloc_scan_kernel(AllocParams p,
     }
   }
   __syncthreads();
-  int requests = 0, pairs = 0, missing = 0;
+  int requests = 0, pairs = 0;
+  long missing = 0, missing_here;         // a row of 2^31 - 1 tokens counts 2^27
   for (int base = 0; base < p.t.batch; base += kScanThreads) {
     const int b = base + tid;
     int copies = 0, need = 0, over = 0;
@@ -214,8 +208,8 @@ __global__ __launch_bounds__(kScanThreads) void alloc_scan_kernel(AllocParams p,
     const bool gets = copies && before < free;           // a row's copy is its first request
     const int place = pairs + block_before<kScanThreads>(gets ? 1 : 0, &all);
     pairs += all;
-    block_before<kScanThreads>(over, &all);
-    missing += all;
+    block_before<kScanThreads>(long(over), &missing_here);
+    missing += missing_here;
     if (b < p.t.batch) {
       p.row_base[b] = before;
       p.row_pair[b] = gets ? place : -1;
@@ -228,7 +222,7 @@ __global__ __launch_bounds__(kScanThreads) void alloc_scan_kernel(AllocParams p,
   }
   if (tid == 0) {
     p.counts[0] = pairs;
-    p.counts[1] = missing + max(requests - free, 0);
+    p.counts[1] = int(min(missing + max(requests - free, 0), 2147483647l));
   }
 }
 
