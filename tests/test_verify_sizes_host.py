@@ -1,0 +1,28 @@
+"""Numbers beyond the C interface's int (no GPU): ctypes would pass their low 32
+bits."""
+import pytest
+import torch
+
+import w4a8_gemm_amd as w4
+from test_int_range_host import BIG, calls, fake, state  # noqa: F401  (calls: a fixture)
+
+pytestmark = pytest.mark.filterwarnings("ignore:Accessing the data pointer of FakeTensor")
+i32 = torch.int32
+
+
+def row(n):
+    return fake((n,), (1,), i32)
+
+
+def test_page_sizes(calls):
+    _, _, table, lens = state()
+    refs = row(9)
+    for page in (BIG + 16, BIG, -BIG + 16, -16, 2 ** 31):
+        for bad in (lambda: w4.kv_fork(table, lens, refs, row(2), page), lambda: w4.kv_alloc(table, lens, refs, 1, page),
+                    lambda: w4.kv_alloc(table, lens, refs, row(2), page)):
+            with pytest.raises(ValueError):
+                bad()
+    assert not calls
+    w4.kv_fork(table, lens, refs, row(2), 16)
+    w4.kv_alloc(table, lens, refs, 1, 16)
+    assert calls[0][7] == calls[1][7] == 16

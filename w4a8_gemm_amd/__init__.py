@@ -879,6 +879,7 @@ def kv_fork(block_table, seq_lens, refs, parent, page_size: int, stream=None):
     pages = _pool_refs(refs, dev)
     rows = parent.shape[0] if parent.dim() == 1 else -1
     _vector("parent", parent, torch.int32, dev, rows)
+    _int("page_size", page_size)
     new = lambda *shape: _empty(shape, torch.int32, block_table.device, stream)
     table, lens, counts = new(rows, width), new(rows), new(pages)
     _check(lib.w4a8_kv_fork(block_table.data_ptr(), ld, width, seq_lens.data_ptr(), batch, refs.data_ptr(), pages,
@@ -902,6 +903,7 @@ def kv_alloc(block_table, seq_lens, refs, tokens, page_size: int, stream=None):
         _vector("tokens", tokens, torch.int32, dev, batch)
     else:
         _int("tokens", tokens)
+    _int("page_size", page_size)
     new = lambda *shape: _empty(shape, torch.int32, block_table.device, stream)
     table, lens, owners, src, dst, counts = new(batch, width), new(batch), new(pages), new(batch), new(batch), new(2)
     need = lib.w4a8_kv_alloc_workspace_size(batch, pages)
