@@ -26,3 +26,15 @@ def test_page_sizes(calls):
     w4.kv_fork(table, lens, refs, row(2), 16)
     w4.kv_alloc(table, lens, refs, 1, 16)
     assert calls[0][7] == calls[1][7] == 16
+
+
+def test_lengths_of_tensors(calls):
+    _, _, table, lens = state()
+    cache, scale = state()[:2]
+    nodes = row(BIG + 3)
+    for bad in (lambda: w4.tree_mask(nodes, row(3), cu_q=row(4), max_q=7), lambda: w4.tree_mask(row(3), nodes, cu_q=row(BIG + 4)),
+                lambda: w4.tree_accept(nodes, nodes, nodes, row(3), cu_q=row(4), max_q=7),
+                lambda: w4.kv_fork(table, lens, row(9), nodes, 16), lambda: w4.kv_copy_pages(cache, scale, nodes, nodes)):
+        with pytest.raises(ValueError):
+            bad()
+    assert not calls

@@ -685,6 +685,8 @@ def _tree(parents, seq_lens, cu_q, dev):
         _vector("cu_q", cu_q, torch.int32, dev, batch + 1)
     elif tokens != batch:
         raise ValueError(f"without cu_q each of the {batch} sequences has one node, got {tokens}")
+    if max(tokens, batch) > INT_MAX:
+        _int("nodes or sequences", max(tokens, batch))
     return tokens, batch
 
 
@@ -879,6 +881,7 @@ def kv_fork(block_table, seq_lens, refs, parent, page_size: int, stream=None):
     pages = _pool_refs(refs, dev)
     rows = parent.shape[0] if parent.dim() == 1 else -1
     _vector("parent", parent, torch.int32, dev, rows)
+    _int("rows", rows)
     _int("page_size", page_size)
     new = lambda *shape: _empty(shape, torch.int32, block_table.device, stream)
     table, lens, counts = new(rows, width), new(rows), new(pages)
@@ -949,6 +952,7 @@ def kv_copy_pages(cache, scale, src, dst, count=None, stream=None):
     pairs = src.shape[0] if src.dim() == 1 else -1
     _vector("src", src, torch.int32, dev, pairs)
     _vector("dst", dst, torch.int32, dev, pairs)
+    _int("pairs", pairs)
     if count is not None and (count.dtype is not torch.int32 or count.numel() < 1 or count.get_device() != dev):
         raise ValueError(f"count: expected an int32 CUDA tensor on device {dev}")
     _check(lib.w4a8_kv_copy_pages(
