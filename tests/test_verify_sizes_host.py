@@ -38,3 +38,15 @@ def test_lengths_of_tensors(calls):
         with pytest.raises(ValueError):
             bad()
     assert not calls
+
+
+@pytest.mark.parametrize("name", ["max_q", "max_len", "window"])
+def test_bounds_below_the_range(calls, name):
+    """They reach the library negative, which refuses them."""
+    q = fake((2, 4, 64), (256, 64, 1))
+    for value in (-1, -2 ** 31, -BIG, -BIG + 5, -2 ** 31 - 1):
+        w4.paged_attention(q, *state(), **{name: value})
+        w4.tree_attention(q, *state(), fake((2, 1), (1, 1), i32), **{name: value})
+        for args, at in ((calls.pop(-2), (4, 5, 7)), (calls.pop(-1), (7, 8, 10))):
+            passed = args[dict(zip(("max_q", "max_len", "window"), at))[name]]
+            assert -2 ** 31 <= passed < 0

@@ -437,6 +437,14 @@ def _int(name, v):
     return v
 
 
+def _bounds(*values):
+    """A bound or a window beyond any sequence is none; one below 0 is refused by
+    the library."""
+    if max(values) > INT_MAX or min(values) < 0:
+        return tuple(max(-1, min(v, INT_MAX)) for v in values)
+    return values
+
+
 def _ld(t):
     """Row stride of a 2-D tensor (a single row's stride says nothing)."""
     m, k = t.shape
@@ -658,9 +666,7 @@ def paged_attention(q, cache, scale_kv, block_table, seq_lens, cu_q=None, max_q:
         max_len = view.max_pages * view.page_size
     if max_q is None:
         max_q = 1 if cu_q is None else tokens
-    # a bound or a window beyond any sequence is none
-    if max_q > INT_MAX or max_len > INT_MAX or window > INT_MAX:
-        max_q, max_len, window = min(max_q, INT_MAX), min(max_len, INT_MAX), min(window, INT_MAX)
+    max_q, max_len, window = _bounds(max_q, max_len, window)
     need = lib.w4a8_paged_attention_workspace_size(ctypes.byref(view), heads, max_q, max_len)
     if need and workspace is None:
         workspace = _empty(need, torch.uint8, q.device, stream, returned=False)
@@ -751,8 +757,7 @@ def tree_attention(q, cache, scale_kv, block_table, seq_lens, mask, cu_q=None, m
         max_len = view.max_pages * view.page_size
     if max_q is None:
         max_q = 1 if cu_q is None else tokens
-    if max_q > INT_MAX or max_len > INT_MAX or window > INT_MAX:
-        max_q, max_len, window = min(max_q, INT_MAX), min(max_len, INT_MAX), min(window, INT_MAX)
+    max_q, max_len, window = _bounds(max_q, max_len, window)
     need = lib.w4a8_tree_attention_workspace_size(ctypes.byref(view), heads, max_q, max_len)
     if need and workspace is None:
         workspace = _empty(need, torch.uint8, q.device, stream, returned=False)
