@@ -50,3 +50,10 @@ def test_bounds_below_the_range(calls, name):
         for args, at in ((calls.pop(-2), (4, 5, 7)), (calls.pop(-1), (7, 8, 10))):
             passed = args[dict(zip(("max_q", "max_len", "window"), at))[name]]
             assert -2 ** 31 <= passed < 0
+
+
+@pytest.mark.parametrize("pages", [1, 2, 9])
+def test_pairs_of_a_compaction(calls, pages):
+    """Half as many as pages, none of a single one: the kernels write no more."""
+    _, _, src, dst, _ = w4.kv_compact(state()[2], row(pages))[1:]
+    assert src.shape == dst.shape == (pages // 2,)

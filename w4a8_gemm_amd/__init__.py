@@ -934,7 +934,7 @@ def kv_compact(block_table, refs, stream=None):
     batch, width, ld = _table(block_table, dev)
     pages = _pool_refs(refs, dev)
     new = lambda *shape: _empty(shape, torch.int32, block_table.device, stream)
-    moves = max(1, pages // 2)
+    moves = pages // 2
     table, owners, place, src, dst, counts = new(batch, width), new(pages), new(pages), new(moves), new(moves), new(2)
     need = lib.w4a8_kv_compact_workspace_size(pages)
     workspace = _empty(need, torch.uint8, block_table.device, stream, returned=False)
