@@ -647,6 +647,12 @@ w4a8_status w4a8_kv_fork(const int32_t* block_table_dev, int block_table_ld, int
  * first if it is shared (refs > 1): the sequence gets a page of its own and the
  * pair goes to src, dst for w4a8_kv_copy_pages.  All sequences that write a shared
  * page copy it, except the last of them if nobody else holds it.
+ * Entries behind a sequence's tokens must not name a shared page: new tokens that
+ * reach one are given it as it is, whoever else has tokens there.  None does
+ * unless the caller lowers a sequence's length: w4a8_kv_fork shares pages with
+ * tokens only.  A sequence taken back past a shared page gives up the pages behind
+ * its tokens first, by being continued in another row (w4a8_kv_fork with
+ * parent[i] != i).
  *   tokens_dev   [batch] int32 new tokens of each sequence, or NULL: `tokens` each
  *   new_lens_dev [batch], the lengths with them
  *   src_dev, dst_dev  [batch] int32: pairs in the order of sequences, then -1

@@ -901,7 +901,9 @@ def kv_alloc(block_table, seq_lens, refs, tokens, page_size: int, stream=None):
     """Pages for the next tokens (a number, or int32 [batch]) of each sequence:
     (block_table, seq_lens with them, refs, src, dst, counts).  Pages src[i] are to
     be copied to dst[i], for i < counts[0] (kv_copy_pages()); counts[1] entries got
-    no page.  The arguments stay as they are.  See w4a8_kv_alloc."""
+    no page.  A sequence whose length was lowered gives up shared pages behind its
+    tokens before, by a kv_fork() into another row.  The arguments stay as they are.
+    See w4a8_kv_alloc."""
     dev = block_table.get_device()
     batch, width, ld = _table(block_table, dev)
     _vector("seq_lens", seq_lens, torch.int32, dev, batch)
