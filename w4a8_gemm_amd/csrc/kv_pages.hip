@@ -188,14 +188,14 @@ __global__ __launch_bounds__(kScanThreads) void alloc_scan_kernel(AllocParams p,
   }
   __syncthreads();
   int requests = 0, pairs = 0;
-  long missing = 0, missing_here;         // a row of 2^31 - 1 tokens counts 2^27
+  long beyond = 0;                        // a row of 2^31 - 1 tokens counts 2^27
   for (int base = 0; base < p.t.batch; base += kScanThreads) {
     const int b = base + tid;
-    int copies = 0, need = 0, over = 0;
+    int copies = 0, need = 0;
     if (b < p.t.batch) {
       const int page = p.row_held[b];
       need = p.row_need[b];
-      over = p.row_over[b];
+      beyond += p.row_over[b];
       if (page >= 0) {
         const int refs = p.t.refs[page];
         const int writers = __hip_atomic_load(&p.writers[page], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -208,8 +208,6 @@ __global__ __launch_bounds__(kScanThreads) void alloc_scan_kernel(AllocParams p,
     const bool gets = copies && before < free;           // a row's copy is its first request
     const int place = pairs + block_before<kScanThreads>(gets ? 1 : 0, &all);
     pairs += all;
-    block_before<kScanThreads>(long(over), &missing_here);
-    missing += missing_here;
     if (b < p.t.batch) {
       p.row_base[b] = before;
       p.row_pair[b] = gets ? place : -1;
@@ -220,6 +218,8 @@ __global__ __launch_bounds__(kScanThreads) void alloc_scan_kernel(AllocParams p,
     p.src[i] = -1;
     p.dst[i] = -1;
   }
+  long missing = 0;
+  if (__syncthreads_or(beyond != 0)) block_before<kScanThreads>(beyond, &missing);
   if (tid == 0) {
     p.counts[0] = pairs;
     p.counts[1] = int(min(missing + max(requests - free, 0), 2147483647l));
