@@ -6,10 +6,11 @@
 // depend on scheduling: atomics only count, or keep a largest row, and free pages
 // are handed out in ascending order to requests in the order of sequences and
 // positions.  Latency bounds the table operators; copies are bound by memory.
-// Measured: 64 beams in groups of 4 over 500 tokens in pages of 16, forked 6.0 us (two
-// launches), given pages 12.9 (three; the scan over rows, one workgroup, 4.9), 1 MB of
-// shared pages copied 3.7; half of a pool of 1500 pages of 64 KB moved together 12.5
-// (three) and 24.6 MB of it copied 9.6 us, 5.1 TB/s read and written.
+// Measured: 64 beams in groups of 4 over 500 tokens in pages of 16, forked 5.5 us (two
+// launches), given pages 10.7 (three; the scan over rows, one workgroup, 4.9), 1 MB of
+// shared pages copied 3.7; pages of 16 for a prompt of 8192 tokens 60 (a page a turn of
+// the row's wave, 0.1 each), for 16 of 2000 26; half of a pool of 1500 pages of 64 KB
+// moved together 12.5 (three) and 24.6 MB of it copied 9.6 us, 5.1 TB/s read and written.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -735,7 +735,10 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p) {
     const uint64_t target = target_of(all);
     if (upto >= target && upto - mass < target) finish(int(own.y), float(w / double(all)));
   };
-  // The n-th largest of the maxima is not above the n-th largest of all logits.
+  // The n-th largest of the maxima is not above the n-th largest of all logits.  It
+  // bounds well where n is small beside their number, and not at all beyond it: one
+  // row of 32000 normal fp16 logits (500 groups) with top_k 50 16.6 us, 256 45, 400 71,
+  // 499 203, 501 58, 1000 96, 2048 222.
   const bool by_count = s.top_k > 0, by_mass = s.top_p < 1.0f;
   uint32_t at_key;
   uint64_t left;

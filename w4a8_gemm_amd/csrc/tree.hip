@@ -8,8 +8,9 @@
 //
 // All three are latency: a launch and loads that wait for each other.  Measured,
 // graph replays of tree_accept and kv_keep: one tree of 26 nodes, heads 32 / 8 of
-// 128, 6.5 us (2.9 and 4.3 in the kernels); 96 of up to 64 nodes 10.7 (5.7 and 7.1),
-// where the 1.9 MB that are read and written would take 0.4.
+// 128, 6.7 us (2.9 and 4.3 in the kernels); 96 of up to 64 nodes 10.7 (5.7 and 7.1),
+// where the 1.9 MB that are read and written would take 0.4.  tree_mask: one tree of 26
+// 2.7 us, 16 of 64 3.7, 64 chains of 64 12, 6 chains of 200 36 (a load a level).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

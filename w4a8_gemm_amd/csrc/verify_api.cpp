@@ -35,17 +35,25 @@ TreePlan plan_tree(const KvArgs& kv, int q_heads, int max_q, int max_len) {
   const long steps = (long(max_len) + kTreeStep - 1) / kTreeStep;
   // 32 rows a workgroup share the conversion of the codes, 16 leave more
   // workgroups and less to do before and after the keys.  By the products of 16
-  // rows and a step there are: 3500 (one tree of 26 tokens over 2001 keys, heads
-  // 32 / 8) 13.8 us with 16 rows and 16.4 with 32; 43000 (6 of up to 200 over 1700)
-  // 20 and 24; 164000 (16 of up to 64 over 4096) 89 and 73, (4 of 13 over 50000) 86
-  // and 75.  64 rows take too many registers for more than two waves a SIMD and
-  // measured 27, 33, 82 and 72.
+  // rows and a step there are, us with 16 rows and with 32, heads of 128: 3500 (one
+  // tree of 26 tokens over 2001 keys) 13.8 and 16.5; 11000 20.6 and 21.3; 17000 27.6
+  // and 25.1; 33000 (2 trees of 64) 35 and 28.7, (8 of 40) 27.6 and 30.5; 51000 52
+  // and 42; 72000 66 and 53; 111000 74 and 53; 128000 (one of 64 over 30000) 121 and
+  // 68; 169000 (16 of up to 64 over 4096) 89 and 73.  Heads of 64: 43000 (6 of up to
+  // 200 over 1700) 20 and 24; 46000 27.2 and 31.4; 77000 33.9 and 37.9.  One limit
+  // for both: below it heads of 128 lose up to a quarter, above it heads of 64 up to
+  // an eighth.  64 rows take too many registers for more than two waves a SIMD and
+  // measured 27, 33, 82 and 72 on the trees of 3500, 43000 and 169000 products and
+  // on 4 of 13 over 50000 (16 rows 86, 32 75).
   const long products = attn_tiles(kv, group, 16) * kv.kv_heads * steps;
   pl.tiles = rows <= 16 || products < kMuchWork ? 1 : 2;
   // Tiles are split where they do not fill the device and there are keys for
   // two parts of kLeastSteps (one tree over 2001 keys: parts of 8 steps 16.9 us, of
   // 16 13.8).  Three workgroups a unit measured 77 against 73 us on the 16 trees,
-  // 75 and 75 on the long ones.
+  // 75 and 75 on the long ones.  The host knows how many tiles there may be, not how
+  // long each is: where they may fill the device none is split, and a long sequence
+  // among many short ones is one workgroup's a head (64 of 8 nodes, one of them over
+  // 50000 keys, 420 us, and 13.6 with that one over 100).
   const long tiles = attn_tiles(kv, group, 16 * pl.tiles);
   pl.least = kLeastSteps;
   pl.shares = int(std::max(kResident / kv.kv_heads, tiles));
